@@ -86,6 +86,12 @@ _SIGS = {
     "gsz_shard_reduce_mean_noalloc": [_P, _I32, _P, _I32, _P, _P, _P],
     "gsz_allreduce_mean": [_P, _P, _P, _P, _P, ctypes.c_size_t, _P],
     "gsz_adamw_step": [_P, _P, _P, _P, _I64, _P, ctypes.POINTER(AdamWHP), _P, _P],
+    "gsz_dropout": [_P, _P, _P, _I64, _I32, ctypes.c_double, _P, ctypes.c_uint32, _P],
+    "gsz_embedding_lookup": [_P, _I32, _I64, _I64, _P, _I32, _I64, ctypes.c_double, ctypes.c_double,
+                             _P, ctypes.c_uint32, _P, _I32, _P],
+    "gsz_embedding_workspace_bytes": [_I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "gsz_embedding_grad": [_P, _I32, _I64, _P, _I32, _I64, _I64, ctypes.c_double, ctypes.c_double,
+                           _P, ctypes.c_uint32, _P, _I32, _I32, _P, ctypes.c_size_t, _P],
 }
 
 _TEST_SIGS = {"gsz_test_set_grid_limit": [ctypes.c_int64],
@@ -279,6 +285,14 @@ class Plan:
         off, b = _I64(), _I32()
         _check(self._lib.gsz_plan_tensor(self._h, t, ctypes.byref(off), ctypes.byref(b)), self._lib)
         return off.value, b.value
+
+    def view(self, t, flat):
+        """Tensor t's place in a bucket-flat buffer (parameters or gradients, bf16
+        or fp32), as a 1-D view."""
+        off, _ = self.tensor(t)
+        if flat.numel() < self.flat_len:
+            raise ValueError(f"flat has {flat.numel()} elements, the plan needs {self.flat_len}")
+        return flat.view(-1)[off:off + self.numel[t]]
 
     def check(self, peer_hash):
         _check(self._lib.gsz_plan_check(self._h, ctypes.c_uint64(peer_hash)), self._lib)
@@ -547,3 +561,111 @@ def adamw_step(master, m, v, g, coef, hp, out_bf16, stream=None):
                                  _ptr(v, "v", _f32(), min_numel=n), _ptr(g, "g", _f32()), n,
                                  _ptr(coef, "coef", _f32(), min_numel=1), ctypes.byref(hp),
                                  _ptr(out_bf16, "out_bf16", bt, min_numel=n), _stream(stream)))
+
+
+def _value_type(t, name):
+    """GSZ_TYPE_* of a value tensor."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype in _bf16_types():
+        return 0
+    if t.dtype in _f32():
+        return 1
+    raise ValueError(f"{name} has dtype {t.dtype}, expected bf16 (or its bits) or float32")
+
+
+def _id_type(ids):
+    import torch
+    if ids.dtype == torch.int32:
+        return 2
+    if ids.dtype == torch.int64:
+        return 3
+    raise ValueError(f"ids has dtype {ids.dtype}, expected int32 or int64")
+
+
+def _rng_ptr(rng):
+    """{seed, step} on the device, two 64-bit integers."""
+    import torch
+    return _ptr(rng, "rng", (torch.int64, torch.uint64), allow_none=True, numel=2)
+
+
+def _one_device(stream, **tensors):
+    """The stream of a call whose kernels run on the current device: every
+    tensor, and the stream if given as an object, must be there."""
+    import torch
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    where = getattr(stream, "device", None)
+    if where is not None and where.index != dev:
+        raise ValueError(f"stream is on {where}, the current device is cuda:{dev}")
+    return _stream(stream)
+
+
+def _site(site):
+    if not 0 <= site < 1 << 32:
+        raise ValueError(f"site {site} is not a 32-bit number")
+    return site
+
+
+def dropout(x, y, p, rng, site=0, add=None, stream=None):
+    """gsz_dropout: y = (add or 0) + dropout(x) with probability p.  rng: a device
+    tensor of two int64, {seed, step}.  The backward pass is the same call on the
+    gradient."""
+    n = x.numel()
+    vt = _value_type(x, "x")
+    xp = _ptr(x, "x", (x.dtype,))
+    yp = _ptr(y, "y", (x.dtype,), numel=n)
+    ap = _ptr(add, "add", (x.dtype,), allow_none=True, numel=n)
+    rp, site = _rng_ptr(rng), _site(site)
+    st = _one_device(stream, x=x, y=y, add=add, rng=rng)
+    _check(load().gsz_dropout(xp, ap, yp, n, vt, float(p), rp, site, st))
+
+
+def _table_shape(table, name):
+    if table.dim() != 2:
+        raise ValueError(f"{name} must be 2-D (rows, dim), got {table.dim()}-D")
+    return table.shape[0], table.shape[1]
+
+
+def embedding_lookup(ids, table, out, scale=1.0, p=0.0, rng=None, site=0, stream=None):
+    """gsz_embedding_lookup: out[i] = dropout(scale * table[ids[i]]), a zero row where
+    ids[i] is outside the table.  table is 2-D (rows, dim), for instance
+    plan.view(t, gathered).view(rows, dim); out holds ids.numel() * dim values."""
+    rows, dim = _table_shape(table, "table")
+    n = ids.numel()
+    it, tt, ot = _id_type(ids), _value_type(table, "table"), _value_type(out, "out")
+    ip = _ptr(ids, "ids", (ids.dtype,))
+    tp = _ptr(table, "table", (table.dtype,))
+    op = _ptr(out, "out", (out.dtype,), numel=n * dim)
+    rp, site = _rng_ptr(rng), _site(site)
+    st = _one_device(stream, ids=ids, table=table, out=out, rng=rng)
+    _check(load().gsz_embedding_lookup(tp, tt, rows, dim, ip, it, n, float(scale), float(p), rp, site,
+                                       op, ot, st))
+
+
+def embedding_workspace_bytes(n, rows, dim):
+    """Device scratch bytes for embedding_grad of n tokens on a (rows, dim) table."""
+    out = ctypes.c_size_t()
+    _check(load().gsz_embedding_workspace_bytes(int(n), int(rows), int(dim), ctypes.byref(out)))
+    return out.value
+
+
+def embedding_grad(ids, dy, grad, ws, scale=1.0, p=0.0, rng=None, site=0, accumulate=False, stream=None):
+    """gsz_embedding_grad: the gradient of embedding_lookup (same scale, p, rng and
+    site) with respect to its table, written to grad (2-D, rows x dim; for instance
+    plan.view(t, flat).view(rows, dim) of a bf16 or fp32 bucket buffer) or, with
+    accumulate, added to it.  ws: a tensor of at least embedding_workspace_bytes."""
+    rows, dim = _table_shape(grad, "grad")
+    n = ids.numel()
+    it, dt, gt = _id_type(ids), _value_type(dy, "dy"), _value_type(grad, "grad")
+    ip = _ptr(ids, "ids", (ids.dtype,))
+    dp = _ptr(dy, "dy", (dy.dtype,), numel=n * dim)
+    gp = _ptr(grad, "grad", (grad.dtype,))
+    wp = _ptr(ws, "ws", (ws.dtype,) if ws is not None else (), allow_none=True)
+    nbytes = ws.numel() * ws.element_size() if ws is not None else 0
+    rp, site = _rng_ptr(rng), _site(site)
+    st = _one_device(stream, ids=ids, dy=dy, grad=grad, ws=ws, rng=rng)
+    _check(load().gsz_embedding_grad(ip, it, n, dp, dt, rows, dim, float(scale), float(p), rp, site, gp,
+                                     gt, 1 if accumulate else 0, wp, nbytes, st))

@@ -20,9 +20,11 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
          "-ffp-contract=off", "-fno-fast-math",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-Wall", "-Wno-unused-result",
-         "-I", os.path.join(_ROOT, "include"),
+         "-I", os.path.join(_ROOT, "include"), "-I", os.path.join(_HERE, "csrc"),
          "-Wl,-rpath,/opt/rocm/lib"]
-SOURCES = ["csrc/plan.cpp", "csrc/gsz_step.hip"]
+# csrc/ holds the step; layers/ the embedding and dropout kernels around it (the
+# step's counter summaries are keyed to csrc/ alone).
+SOURCES = ["csrc/plan.cpp", "csrc/gsz_step.hip", "layers/gsz_layers.hip"]
 
 
 def build(verbose: bool = False) -> str:

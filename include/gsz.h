@@ -14,6 +14,11 @@
  *      in all-gather layout                         (gsz_shard_adamw_step,
  *                                                    gsz_allgather_layout_write)
  *
+ * and the model's two ends of that step at its embedding: the lookup that reads
+ * the table in place in the gathered parameters, its gradient written or
+ * accumulated in place in a bucket, and the dropout between them
+ * (gsz_embedding_lookup, gsz_embedding_grad, gsz_dropout).
+ *
  * Pages cited (title, section):
  *   "Data parallelism in depth" (infra-guide chapter 4.1)
  *   "Distributed Training: Data Parallel, Model Parallel and FSDP Strategies"
@@ -367,6 +372,87 @@ int gsz_allreduce_mean(const gsz_plan* plan, const uint16_t* const* contrib, flo
 int gsz_adamw_step(float* master, float* m, float* v, const float* g, int64_t n,
                    const float* coef, const gsz_adamw_hp* hp, uint16_t* out_bf16,
                    hipStream_t stream);
+
+/* ------------------------------------------- embedding and dropout --- */
+
+/* Value and id types of the calls below. */
+#define GSZ_TYPE_BF16 0
+#define GSZ_TYPE_F32 1
+#define GSZ_TYPE_I32 2
+#define GSZ_TYPE_I64 3
+
+/* Dropout: y[e] = (add[e] or 0) + (dropped(e) ? 0 : x[e] * k), e in [0, n), in
+ * fp32, rounded once to the values' type (bf16 nearest even).
+ *
+ * The mask is a function of (seed, step, site, e) and never stored: element e
+ * takes a 32-bit number u(e) and is dropped iff u(e) < T = floor(p 2^32);
+ * k = 1 / (1 - T 2^-32), so the expectation is exact.  u(e): half j = e mod 8 (16
+ * bits, low half of the first word first) of the four words of Philox4x32-10 with
+ * key (seed low, seed high) and counter (b low, b high, site, step low), b = e / 8,
+ * is the high half of u; half j at the counter (b low, b high | 2^31, site, step
+ * low) the low half.
+ *
+ * The backward pass is the same call on the gradient of y with the same p, rng,
+ * site and no add (the gradient of add is the gradient of y).  A dropped element
+ * is 0 whatever x holds (infinities and NaN too).
+ *   x, y, add (device, n values of `type`: GSZ_TYPE_BF16 or GSZ_TYPE_F32; any
+ *     address that is a multiple of the value's size); add may be NULL.  y may be
+ *     x or add themselves; it must not overlap them otherwise.
+ *   p: in [0, 1) (GSZ_ERR_INVALID_ARG otherwise).
+ *   rng (device, two uint64: {seed, step}, 8-byte aligned; step is taken mod 2^32):
+ *     read by the kernel, so a captured graph draws a new mask at each replay once
+ *     the step in that memory has moved on.  May be NULL if T = 0.
+ *   site: one number per place of a model that drops.  Ranks that hold different
+ *     samples take different seeds (or sites), or their masks are the same.
+ * GSZ_ERR_SIZE if n > 2^60. */
+int gsz_dropout(const void* x, const void* add, void* y, int64_t n, int32_t type, double p,
+                const uint64_t* rng, uint32_t site, hipStream_t stream);
+
+/* Embedding lookup with scaling and dropout, i in [0, n), c in [0, dim):
+ *   out[i*dim + c] = id_i in [0, rows) and not dropped(i*dim + c)
+ *                    ? table[id_i*dim + c] * c0 : 0,     c0 = scale * k
+ * (the dropout of gsz_dropout over the n * dim elements of out; c0 formed in double
+ * and rounded once; one fp32 multiplication, one rounding to out_type).  An id
+ * outside [0, rows) is no row: padding, or another rank's part of the vocabulary.
+ *   table (device, rows * dim values, GSZ_TYPE_BF16 or GSZ_TYPE_F32): any multiple of
+ *     the value's size, so it may be read where it lies in a bucket-flat buffer (the
+ *     gathered parameters, at gsz_plan_tensor's offset).
+ *   ids (device, n of GSZ_TYPE_I32 or GSZ_TYPE_I64); out (device, n * dim of out_type,
+ *     any multiple of the value's size; must not overlap table or ids).
+ * GSZ_ERR_SIZE if rows or n is over 2^31 - 1 or dim over 2^29;
+ * GSZ_ERR_INVALID_ARG if p is not in [0, 1) or c0 is not finite in fp32. */
+int gsz_embedding_lookup(const void* table, int32_t table_type, int64_t rows, int64_t dim,
+                         const void* ids, int32_t id_type, int64_t n, double scale, double p,
+                         const uint64_t* rng, uint32_t site, void* out, int32_t out_type,
+                         hipStream_t stream);
+
+/* *out = bytes of device scratch gsz_embedding_grad needs for these sizes, per call
+ * in flight (two captured graphs that may run at once need one each): the sorted
+ * tokens and fp32 partial sums of rows with many tokens, at most about one fp32 per
+ * gradient value for small n and an eighth of that for large n.  Needs no
+ * initialisation.  Errors as gsz_embedding_lookup's sizes. */
+int gsz_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim, size_t* out);
+
+/* Gradient of gsz_embedding_lookup with respect to the table:
+ *   grad[v*dim + c] = (accumulate ? grad[v*dim + c] : 0)
+ *                     + c0 * sum over i with id_i = v of (dropped(i*dim + c) ? 0 : dy[i*dim + c])
+ * with the lookup's scale, p, rng and site.  The tokens are sorted by row and each
+ * row's are summed in fp32, in an order that depends on the call's sizes and ids
+ * alone: the same call gives the same bits.  One rounding to grad_type at the end.
+ * accumulate = 0 writes every row (0 where no token has it); accumulate = 1 reads
+ * and writes only the rows that tokens have, as gsz_bucket_accumulate[_f32] adds a
+ * micro-batch to a bucket.  Ids outside [0, rows) add nothing.
+ *   dy (device, n * dim of dy_type); grad (device, rows * dim of grad_type): both any
+ *     multiple of the value's size, so grad may be a tensor's place in a bf16 or fp32
+ *     bucket-flat buffer.  It must not overlap dy or ids.
+ *   ws (device, 16-byte aligned, >= gsz_embedding_workspace_bytes): scratch, required
+ *     unless n or dim is 0 (GSZ_ERR_SIZE if too small).
+ * Errors as gsz_embedding_lookup; GSZ_ERR_SIZE too if a launch would need more than
+ * 2^31 work-items (n * dim over about 2^39, or n over 2^29). */
+int gsz_embedding_grad(const void* ids, int32_t id_type, int64_t n, const void* dy, int32_t dy_type,
+                       int64_t rows, int64_t dim, double scale, double p, const uint64_t* rng,
+                       uint32_t site, void* grad, int32_t grad_type, int32_t accumulate, void* ws,
+                       size_t ws_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------ errors --- */
 

@@ -1,0 +1,163 @@
+"""Host-side checks of the embedding and dropout entry points: what they refuse
+before any device call, through the binding and through the C ABI."""
+import ctypes
+import os
+import re
+
+import pytest
+
+import gradient_sync_zero_amd as G
+
+LAYERS = os.path.join(os.path.dirname(G.LIB_PATH), "layers")
+BF16, F32, I32, I64 = 0, 1, 2, 3
+INVALID, MISALIGNED, SIZE = -1, -2, -3
+BUF = 1 << 20                    # an aligned address that no refused call reads
+
+
+def lookup(lib, table=BUF, tt=BF16, rows=10, dim=8, ids=BUF, it=I64, n=4, scale=1.0, p=0.0, rng=None,
+           site=0, out=BUF, ot=BF16):
+    return lib.gsz_embedding_lookup(table, tt, rows, dim, ids, it, n, scale, p, rng, site, out, ot, None)
+
+
+def grad(lib, ids=BUF, it=I64, n=4, dy=BUF, dt=BF16, rows=10, dim=8, scale=1.0, p=0.0, rng=None, site=0,
+         g=BUF, gt=BF16, acc=0, ws=BUF, ws_bytes=1 << 30):
+    return lib.gsz_embedding_grad(ids, it, n, dy, dt, rows, dim, scale, p, rng, site, g, gt, acc, ws,
+                                  ws_bytes, None)
+
+
+def drop(lib, x=BUF, add=None, y=BUF, n=16, t=BF16, p=0.1, rng=BUF, site=0):
+    return lib.gsz_dropout(x, add, y, n, t, p, rng, site, None)
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("call,kw,want", [
+    (lookup, dict(tt=2), INVALID), (lookup, dict(ot=-1), INVALID), (lookup, dict(it=F32), INVALID),
+    (lookup, dict(rows=-1), INVALID), (lookup, dict(dim=-1), INVALID), (lookup, dict(n=-1), INVALID),
+    (lookup, dict(rows=1 << 31), SIZE), (lookup, dict(n=1 << 31), SIZE), (lookup, dict(dim=(1 << 29) + 1), SIZE),
+    (lookup, dict(p=1.0), INVALID), (lookup, dict(p=-1e-9), INVALID), (lookup, dict(p=NAN), INVALID),
+    (lookup, dict(p=0.5, rng=None), INVALID), (lookup, dict(p=0.5, rng=BUF + 4), MISALIGNED),
+    (lookup, dict(scale=INF), INVALID), (lookup, dict(scale=NAN), INVALID), (lookup, dict(scale=1e39), INVALID),
+    (lookup, dict(scale=1e38, p=0.999, rng=BUF), INVALID),
+    (lookup, dict(table=None), INVALID), (lookup, dict(ids=None), INVALID), (lookup, dict(out=None), INVALID),
+    (lookup, dict(table=BUF + 1), MISALIGNED), (lookup, dict(tt=F32, table=BUF + 2), MISALIGNED),
+    (lookup, dict(out=BUF + 1), MISALIGNED), (lookup, dict(ids=BUF + 4), MISALIGNED),
+    (lookup, dict(it=I32, ids=BUF + 2), MISALIGNED),
+    (grad, dict(dt=3), INVALID), (grad, dict(gt=9), INVALID), (grad, dict(it=BF16), INVALID),
+    (grad, dict(rows=-1), INVALID), (grad, dict(n=-5), INVALID), (grad, dict(dim=-8), INVALID),
+    (grad, dict(rows=1 << 31), SIZE), (grad, dict(n=1 << 31), SIZE), (grad, dict(dim=1 << 30), SIZE),
+    (grad, dict(acc=2), INVALID), (grad, dict(p=1.5), INVALID), (grad, dict(p=0.1), INVALID),
+    (grad, dict(scale=-INF), INVALID), (grad, dict(dy=None), INVALID), (grad, dict(ids=None), INVALID),
+    (grad, dict(g=None), INVALID), (grad, dict(ws=None), SIZE), (grad, dict(ws_bytes=16), SIZE),
+    (grad, dict(ws=BUF + 8), MISALIGNED), (grad, dict(dy=BUF + 1), MISALIGNED),
+    (grad, dict(gt=F32, g=BUF + 2), MISALIGNED), (grad, dict(ids=BUF + 4), MISALIGNED),
+    # more work-items than one launch holds: refused before the sort is enqueued
+    (grad, dict(n=(1 << 31) - 1, ws_bytes=1 << 62), SIZE),
+    (drop, dict(t=2), INVALID), (drop, dict(n=-1), INVALID), (drop, dict(n=(1 << 60) + 1), SIZE),
+    (drop, dict(p=1.0), INVALID), (drop, dict(p=NAN), INVALID), (drop, dict(rng=None), INVALID),
+    (drop, dict(rng=BUF + 4), MISALIGNED), (drop, dict(x=None), INVALID), (drop, dict(y=None), INVALID),
+    (drop, dict(x=BUF + 1), MISALIGNED), (drop, dict(t=F32, y=BUF + 2), MISALIGNED),
+    (drop, dict(add=BUF + 1), MISALIGNED),
+])
+def test_refusals(call, kw, want):
+    lib = G.load()
+    assert call(lib, **kw) == want, (lib.gsz_last_error(), kw)
+    assert lib.gsz_last_error().startswith((b"gsz_embedding", b"gsz_dropout"))
+
+
+def test_workspace_bytes():
+    assert G.embedding_workspace_bytes(0, 0, 0) >= 0
+    for n, rows, dim in ((1, 1, 1), (8192, 50257, 768), (8193, 50257, 768), (65536, 32000, 8192),
+                         (300_000, 5, 4), (1 << 22, 1 << 30, 1)):
+        b = G.embedding_workspace_bytes(n, rows, dim)
+        assert b % 256 == 0 and b >= 8 * n
+        # sorted pairs twice, three digit tables, two fp32 partial rows per chunk of at least 8 tokens
+        assert b <= 16 * n + 3 * 4 * 256 * 1024 + 8 * (-(-n // 8)) * (dim + 7) + 4096
+    for bad in ((-1, 1, 1), (1, -1, 1), (1, 1, -1), (1 << 31, 1, 1), (1, 1 << 31, 1), (1, 1, 1 << 30)):
+        with pytest.raises(G.GszError):
+            G.embedding_workspace_bytes(*bad)
+    assert G.load().gsz_embedding_workspace_bytes(1, 1, 1, None) == INVALID
+
+
+def test_binding_refusals():
+    """Wrong types, shapes, sizes and host tensors never reach the library."""
+    import torch
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt)
+    ids, table, out = z(4, dt=torch.int64), z(10, 8), z(4, 8)
+    for args in ((ids.float(), table, out), (ids, table.half(), out), (ids, table, out.double()),
+                 (ids, table.view(-1), out), (ids, table, out), (None, table, out)):
+        with pytest.raises((ValueError, AttributeError)):
+            G.embedding_lookup(*args, stream=0)
+    for args in ((ids, out.half(), table, out), (ids, out, table.view(-1), out), (ids, out, table, out)):
+        with pytest.raises(ValueError):
+            G.embedding_grad(*args, stream=0)
+    with pytest.raises(ValueError, match="device tensor"):
+        G.dropout(out, out, 0.1, z(2, dt=torch.int64), stream=0)
+    with pytest.raises(ValueError, match="dtype"):
+        G.dropout(out.half(), out.half(), 0.1, z(2, dt=torch.int64), stream=0)
+
+
+class Dev:
+    """Stands in for a device tensor in the binding's checks; it has no storage."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype):
+        self.shape, self.dtype = tuple(shape), dtype
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+    def element_size(self):
+        return 4
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0
+
+
+def test_binding_checks_lengths():
+    import torch
+    bf, f32, i64 = torch.bfloat16, torch.float32, torch.int64
+    ids, table, rng = Dev((2, 3), i64), Dev((10, 8), bf), Dev((2,), i64)
+    with pytest.raises(ValueError, match="out has 47 elements"):
+        G.embedding_lookup(ids, table, Dev((47,), bf), stream=0)
+    with pytest.raises(ValueError, match="dy has 49 elements"):
+        G.embedding_grad(ids, Dev((49,), bf), table, None, stream=0)
+    with pytest.raises(ValueError, match="rng has 3 elements"):
+        G.embedding_lookup(ids, table, Dev((6, 8), f32), p=0.1, rng=Dev((3,), i64), stream=0)
+    with pytest.raises(ValueError, match="y has 5 elements"):
+        G.dropout(Dev((4,), bf), Dev((5,), bf), 0.1, rng, stream=0)
+    with pytest.raises(ValueError, match="y has dtype"):
+        G.dropout(Dev((4,), bf), Dev((4,), f32), 0.1, rng, stream=0)
+    with pytest.raises(ValueError, match="add has 3 elements"):
+        G.dropout(Dev((4,), bf), Dev((4,), bf), 0.1, rng, add=Dev((3,), bf), stream=0)
+    for site in (-1, 1 << 32):
+        with pytest.raises(ValueError, match="site"):
+            G.dropout(Dev((4,), bf), Dev((4,), bf), 0.1, rng, site=site, stream=0)
+
+
+def test_plan_view_is_the_tensors_place():
+    import torch
+    plan = G.Plan([1000, 37, 0, 4096], 4000, 4)
+    flat = torch.arange(plan.flat_len, dtype=torch.float32)
+    for t, n in enumerate(plan.numel):
+        v = plan.view(t, flat)
+        assert v.numel() == n and (n == 0 or int(v[0]) == plan.tensor(t)[0])
+    with pytest.raises(ValueError):
+        plan.view(0, flat[:-1])
+
+
+def test_layers_neither_allocate_nor_wait():
+    banned = re.compile(r"\b(hipMalloc\w*|hipFree\w*|hipExtMalloc\w*|hipHostMalloc|hipDeviceSynchronize|"
+                        r"hipStreamSynchronize|hipEventSynchronize|hipMemcpy\w*|hipMemset\w*)\s*\(")
+    for name in sorted(os.listdir(LAYERS)):
+        assert not banned.search(open(os.path.join(LAYERS, name)).read()), name
