@@ -29,6 +29,7 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 // 16-byte vectors at any element's place: tensors lie anywhere in a flat bucket,
 // and gfx950 takes such accesses whole (unaligned access is part of its HSA ABI).
 typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_at2 __attribute__((aligned(2)));
 typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
 
 // Two fp32 values to bf16, nearest even, the first in the low half
@@ -139,26 +140,26 @@ __device__ __forceinline__ void drop_numbers(const DropKey& d, uint64_t block, u
     }
 }
 
-// a[j] <- 0 where element first + j is dropped (chosen, not multiplied: an
-// infinity or NaN in a dropped place leaves 0).
-__device__ __forceinline__ void drop8(const DropKey& d, uint64_t first, float a[8]) {
-    uint32_t u[8];
+// Bit j: element first + j is dropped.
+__device__ __forceinline__ uint32_t dropped8(const DropKey& d, uint64_t first) {
+    uint32_t u[8], m = 0;
     drop_numbers(d, first >> 3, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m |= (uint32_t)(u[j] < d.threshold) << j;
     const uint32_t s = (uint32_t)first & 7;
-    if (s == 0) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = u[j] < d.threshold ? 0.0f : a[j];
-    } else {                                     // the eight lie in two blocks
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m |= (uint32_t)(u[j] < d.threshold) << j;
+    if (s != 0) {                                // the eight lie in two blocks
         drop_numbers(d, (first >> 3) + 1, u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) m |= (uint32_t)(u[j] < d.threshold) << (8 + j);
-        m >>= s;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = (m >> j & 1) ? 0.0f : a[j];
+        m = m >> s & 0xFFu;
     }
+    return m;
+}
+// a[j] <- 0 where bit j is set (chosen, not multiplied: an infinity or NaN in a
+// dropped place leaves 0).
+__device__ __forceinline__ void drop8(uint32_t gone, float a[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = (gone >> j & 1) ? 0.0f : a[j];
 }
 
 // --------------------------------------------------------------- dropout --
@@ -176,19 +177,23 @@ __global__ __launch_bounds__(kDropBlock) void k_dropout(const T* x, const T* add
     for (int64_t e = (int64_t)blockIdx.x * (8 * kDropBlock) + 8 * threadIdx.x; e < n; e += stride) {
         const int64_t left = n - e;
         float a[8], b[8];
+        Raw8<T> r, q{};
         if (left >= 8) {
-            const Raw8<T> r = load8<true>(x + e);
-            Raw8<T> q{};
+            r = load8<true>(x + e);
             if (ADD) q = load8<true>(add + e);
-            widen(r, a);
-            if (ADD) widen(q, b);
         } else {
-            widen(load8_part(x + e, (int)left), a);
-            if (ADD) widen(load8_part(add + e, (int)left), b);
+            r = load8_part(x + e, (int)left);
+            if (ADD) q = load8_part(add + e, (int)left);
         }
+        uint32_t u[8];
+        if (DROP) drop_numbers(d, (uint64_t)e >> 3, u);      // while the loads are on their way
+        widen(r, a);
+        if (ADD) widen(q, b);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = a[j] * k;
-        if (DROP) drop8(d, (uint64_t)e, a);
+        for (int j = 0; j < 8; ++j) {
+            a[j] = a[j] * k;
+            if (DROP) a[j] = u[j] < d.threshold ? 0.0f : a[j];
+        }
         if (ADD) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) a[j] = b[j] + a[j];

@@ -21,23 +21,29 @@ __device__ __forceinline__ uint32_t row_of(const Ids& ids, int64_t i) {
 // ---------------------------------------------------------------- lookup --
 
 // out[i, c] = id_i is a row and not dropped(i * dim + c) ? table[id_i, c] * c0 : 0.
-// A block takes tile_rows rows of vpr = ceil(dim / 8) vectors, about kLookVecs of
-// them: kLookUnroll loads of the table in flight per lane, then the stores.
-// magic = floor(2^32 / vpr) + 1: (q * magic) >> 32 == q / vpr for q < kLookVecs and
-// vpr <= kLookVecs; wider rows come one to a block.
+// A row is vpr = ceil(dim / 8) vectors, cut into `slices` column slices of at most sv
+// vectors; a block takes tile_rows rows of one slice, up to kLookVecs vectors, with
+// kLookUnroll loads of the table in flight per lane and then the stores.  Block b has
+// slice b mod slices: blocks go to the eight XCDs in turn, so with eight slices each
+// XCD's L2 holds its own columns of the rows that come often, eight times as many
+// rows as if every XCD read whole ones.
+// magic = floor(2^32 / sv) + 1: (q * magic) >> 32 == q / sv for q, sv <= kLookVecs;
+// wider slices come one row to a block.
 constexpr int kLookBlock = 256, kLookUnroll = 4, kLookVecs = kLookBlock * kLookUnroll;
+struct LookShape { int64_t n, dim, vpr, sv, tiles; uint64_t magic; int slices, tile_rows; };
+
 template <typename T, typename O, bool DROP>
-__global__ __launch_bounds__(kLookBlock) void k_lookup(const T* __restrict__ table, Ids ids, int64_t n,
-                                                       int64_t dim, int64_t vpr, int tile_rows,
-                                                       uint64_t magic, float c0, DropArgs da,
-                                                       O* __restrict__ out) {
+__global__ __launch_bounds__(kLookBlock) void k_lookup(const T* __restrict__ table, Ids ids, LookShape s,
+                                                       float c0, DropArgs da, O* __restrict__ out) {
     DropKey d{};
     if (DROP) d = drop_key(da);
-    const int64_t tiles = (n + tile_rows - 1) / tile_rows;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int64_t row0 = tile * tile_rows;
-        const int64_t nrows = n - row0 < tile_rows ? n - row0 : tile_rows;
-        const int64_t vecs = nrows * vpr;
+    const int64_t blocks = s.tiles * s.slices;
+    for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
+        const int64_t tile = s.slices == 1 ? b : b / s.slices, v0 = s.slices == 1 ? 0 : (b % s.slices) * s.sv;
+        const int64_t width = s.vpr - v0 < s.sv ? s.vpr - v0 : s.sv;      // vectors of this slice
+        const int64_t row0 = tile * s.tile_rows;
+        const int64_t nrows = s.n - row0 < s.tile_rows ? s.n - row0 : s.tile_rows;
+        const int64_t vecs = nrows * s.sv;
         for (int64_t q0 = threadIdx.x; q0 < vecs; q0 += kLookVecs) {
             Raw8<T> r[kLookUnroll];
             int64_t row[kLookUnroll], col[kLookUnroll];
@@ -47,17 +53,32 @@ __global__ __launch_bounds__(kLookBlock) void k_lookup(const T* __restrict__ tab
                 const int64_t q = q0 + u * kLookBlock;
                 is_row[u] = false;
                 row[u] = -1;
+                col[u] = 0;
                 if (q < vecs) {
-                    const int64_t lr = tile_rows == 1 ? 0 : (int64_t)(((uint64_t)q * magic) >> 32);
-                    row[u] = row0 + lr;
-                    col[u] = 8 * (q - lr * vpr);
-                    const uint32_t v = row_of(ids, row[u]);
-                    is_row[u] = v != ids.rows;
-                    if (is_row[u]) {
-                        const T* p = table + (int64_t)v * dim + col[u];
-                        const int64_t left = dim - col[u];
-                        r[u] = left >= 8 ? load8<false>(p) : load8_part(p, (int)left);
+                    const int64_t lr = s.tile_rows == 1 ? 0 : (int64_t)(((uint64_t)q * s.magic) >> 32);
+                    const int64_t v = q - lr * s.sv;
+                    if (v < width) {
+                        row[u] = row0 + lr;
+                        col[u] = 8 * (v0 + v);
+                        const uint32_t id = row_of(ids, row[u]);
+                        is_row[u] = id != ids.rows;
+                        if (is_row[u]) {
+                            const T* p = table + (int64_t)id * s.dim + col[u];
+                            const int64_t left = s.dim - col[u];
+                            r[u] = left >= 8 ? load8<false>(p) : load8_part(p, (int)left);
+                        }
                     }
+                }
+            }
+            // The masks need no data: they are drawn while the loads are on their way, in
+            // a loop of its own that holds the generator's code once.
+            uint32_t gone = 0;
+            if (DROP) {
+#pragma unroll 1
+                for (int u = 0; u < kLookUnroll && q0 + u * kLookBlock < vecs; ++u) {
+                    const int64_t q = q0 + u * kLookBlock;
+                    const int64_t lr = s.tile_rows == 1 ? 0 : (int64_t)(((uint64_t)q * s.magic) >> 32);
+                    gone |= dropped8(d, (uint64_t)((row0 + lr) * s.dim + 8 * (v0 + q - lr * s.sv))) << 8 * u;
                 }
             }
 #pragma unroll
@@ -68,15 +89,56 @@ __global__ __launch_bounds__(kLookBlock) void k_lookup(const T* __restrict__ tab
                     widen(r[u], a);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) a[j] = a[j] * c0;
-                    if (DROP) drop8(d, (uint64_t)(row[u] * dim + col[u]), a);
+                    if (DROP) drop8(gone >> 8 * u, a);
                 }
-                O* p = out + row[u] * dim + col[u];
-                const int64_t left = dim - col[u];
+                O* p = out + row[u] * s.dim + col[u];
+                const int64_t left = s.dim - col[u];
                 if (left >= 8) store8<true>(p, a);
                 else store8_part(p, a, (int)left);
             }
         }
     }
+}
+
+// ------------------------------------------------------------- clearing --
+//
+// With accumulate = 0 the rows without a token are cleared.  No launch does only
+// that: the blocks that clear ride along with the sort, whose few blocks leave
+// the memory idle.
+
+// Clears the rows r0 + i, i a set bit of `missing`, with the whole block.
+template <typename G>
+__device__ __forceinline__ void clear_rows(G* __restrict__ grad, int64_t dim, int64_t r0, uint64_t missing) {
+    const float zero[8] = {};
+    for (uint64_t m = missing; m; m &= m - 1) {
+        G* p = grad + (r0 + __builtin_ctzll(m)) * dim;
+        for (int64_t c = 8 * (int64_t)threadIdx.x; c < dim; c += 8 * (int64_t)blockDim.x) {
+            if (dim - c >= 8) store8<true>(p + c, zero);
+            else store8_part(p + c, zero, (int)(dim - c));
+        }
+    }
+}
+
+// Which part of the table a launch clears: `per` rows (at most 64) for each of its
+// blocks from `first_block` on, rows [row0, row1).
+struct ClearShape { void* grad; int64_t dim, row0, row1; unsigned first_block; int per, f32; };
+
+// owner[v] is some token of row v, if there is one: k_count stores every token's
+// position there, and whichever store lands last is as good as another.  The array
+// is never cleared: what it holds counts only if that token does have row v.
+__device__ __forceinline__ void clear_block(const ClearShape& c, const Ids& ids, int64_t n,
+                                            const uint32_t* __restrict__ owner) {
+    const int64_t r0 = c.row0 + (int64_t)(blockIdx.x - c.first_block) * c.per;
+    const int lane = threadIdx.x & 63;
+    const int64_t v = r0 + lane;
+    bool missing = lane < c.per && v < c.row1;
+    if (missing) {
+        const uint32_t i = owner[v];
+        missing = !(i < (uint64_t)n && row_of(ids, i) == (uint32_t)v);
+    }
+    const uint64_t m = __ballot(missing);
+    if (c.f32) clear_rows(static_cast<float*>(c.grad), c.dim, r0, m);
+    else clear_rows(static_cast<uint16_t*>(c.grad), c.dim, r0, m);
 }
 
 // ------------------------------------------------------------------ sort --
@@ -86,161 +148,226 @@ __global__ __launch_bounds__(kLookBlock) void k_lookup(const T* __restrict__ tab
 
 // n <= kRankMax tokens in one launch: token i goes to place
 // #{j : key_j < key_i} + #{j < i : key_j == key_i}.  A block holds all keys in LDS
-// and places 64 tokens; its waves compare them with a slice of the keys each.
-constexpr int kRankMax = 8192, kRankBlock = 512, kRankWaves = kRankBlock / 64;
+// and places kRankTokens tokens; each half of each wave compares them with a slice of
+// the keys.  With PACKED (rows < 2^19) a key and its position are one 32-bit number
+// and a comparison is two instructions.  Every block also clears the rows without a
+// token among clear.per * 64 rows, which it finds among the keys it holds.
+constexpr int kRankMax = 8192, kRankBits = 13, kRankBlock = 1024, kRankTokens = 32;
+constexpr int kRankSlices = kRankBlock / kRankTokens;
+constexpr int64_t kRankPackedRows = (int64_t)1 << (32 - kRankBits);
+template <bool PACKED>
 __global__ __launch_bounds__(kRankBlock) void k_rank(Ids ids, int n, uint32_t* __restrict__ key,
-                                                     uint32_t* __restrict__ pos) {
+                                                     uint32_t* __restrict__ pos, ClearShape clear) {
     __shared__ __align__(16) uint32_t all[kRankMax];
-    __shared__ uint32_t part[kRankWaves][64];
-    const int n4 = (n + 4 * kRankWaves - 1) / (4 * kRankWaves) * (4 * kRankWaves);
-    for (int j = threadIdx.x; j < n4; j += kRankBlock) all[j] = j < n ? row_of(ids, j) : 0xFFFFFFFFu;
-    __syncthreads();
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int i = blockIdx.x * 64 + lane;
-    const uint32_t mine = i < n ? all[i] : 0;
-    const int j0 = wave * (n4 / kRankWaves), j1 = j0 + n4 / kRankWaves;
-    uint32_t less = 0;
-    const u32x4* all4 = reinterpret_cast<const u32x4*>(all);
-    for (int j = j0; j < j1; j += 4) {
-        const u32x4 k = all4[j >> 2];
-        less += (k.x < mine) | ((k.x == mine) & (j < i));
-        less += (k.y < mine) | ((k.y == mine) & (j + 1 < i));
-        less += (k.z < mine) | ((k.z == mine) & (j + 2 < i));
-        less += (k.w < mine) | ((k.w == mine) & (j + 3 < i));
+    __shared__ uint32_t part[kRankSlices][kRankTokens + 1];
+    __shared__ uint32_t seen[64][2];
+    const int tid = threadIdx.x;
+    const int quads = (n + 4 * kRankSlices - 1) / (4 * kRankSlices) * kRankSlices;
+    for (int j = tid; j < 4 * quads; j += kRankBlock) {
+        uint32_t k = 0xFFFFFFFFu;
+        if (j < n) {
+            k = row_of(ids, j);
+            if (PACKED) k = k << kRankBits | (uint32_t)j;
+        }
+        all[j] = k;
     }
-    part[wave][lane] = less;
+    if (tid < 128) seen[tid >> 1][tid & 1] = 0;
     __syncthreads();
-    if (wave == 0 && i < n) {
-        uint32_t s = 0;
+    const int t = tid % kRankTokens, slice = tid / kRankTokens;
+    const int i = blockIdx.x * kRankTokens + t;
+    if ((int64_t)blockIdx.x * kRankTokens < n) {
+        const uint32_t mine = i < n ? all[i] : 0;
+        const u32x4* all4 = reinterpret_cast<const u32x4*>(all);
+        uint32_t less = 0;
+#pragma unroll 4
+        for (int q = slice; q < quads; q += kRankSlices) {
+            const u32x4 k = all4[q];
+            if (PACKED) {
+                less += k.x < mine;
+                less += k.y < mine;
+                less += k.z < mine;
+                less += k.w < mine;
+            } else {
+                const int j = 4 * q;
+                less += (k.x < mine) | ((k.x == mine) & (j < i));
+                less += (k.y < mine) | ((k.y == mine) & (j + 1 < i));
+                less += (k.z < mine) | ((k.z == mine) & (j + 2 < i));
+                less += (k.w < mine) | ((k.w == mine) & (j + 3 < i));
+            }
+        }
+        part[slice][t] = less;
+        __syncthreads();
+        if (slice == 0 && i < n) {
+            uint32_t s = 0;
 #pragma unroll
-        for (int w = 0; w < kRankWaves; ++w) s += part[w][lane];
-        key[s] = mine;
-        pos[s] = (uint32_t)i;
+            for (int w = 0; w < kRankSlices; ++w) s += part[w][t];
+            key[s] = PACKED ? mine >> kRankBits : mine;
+            pos[s] = (uint32_t)i;
+        }
+    }
+    if (!clear.grad) return;
+    // seen: 64 words of 64 rows each
+    const int64_t r0 = (int64_t)blockIdx.x * clear.per * 64;
+    for (int j = tid; j < n; j += kRankBlock) {
+        const int64_t v = (int64_t)(PACKED ? all[j] >> kRankBits : all[j]) - r0;
+        if (v >= 0 && v < (int64_t)clear.per * 64) atomicOr(&seen[v >> 6][v >> 5 & 1], 1u << (v & 31));
+    }
+    __syncthreads();
+    for (int w = 0; w < clear.per; ++w) {
+        const int64_t r = r0 + 64 * w, count = clear.row1 - r;
+        if (count <= 0) break;
+        uint64_t m = ~((uint64_t)seen[w][1] << 32 | seen[w][0]);
+        if (count < 64) m &= ((uint64_t)1 << count) - 1;
+        if (clear.f32) clear_rows(static_cast<float*>(clear.grad), clear.dim, r, m);
+        else clear_rows(static_cast<uint16_t*>(clear.grad), clear.dim, r, m);
     }
 }
 
-// More tokens: stable counting passes over digits of the key, lowest first.
-// count[tile][digit] holds how often a digit occurs in a tile of tokens.
+// More tokens: stable counting passes over digits of the key, lowest first, a launch
+// to count and one to place each.  count[tile][digit]: how often a digit occurs in a
+// tile of `rounds` times kSortTile tokens.  (Counting the next digit while placing this
+// one, with an atomic per token where it lands, saved a launch and cost 10 us of
+// atomics on 16 Ki tokens.)
 constexpr int kSortBlock = 256, kSortWaves = kSortBlock / 64, kSortMaxBins = 1024;
-struct Digit { int shift, bins; };       // bins a power of two
-__device__ __forceinline__ uint32_t digit_of(const Digit& d, uint32_t key) {
-    return (key >> d.shift) & (uint32_t)(d.bins - 1);
+constexpr int kSortPer = 4, kSortTile = kSortBlock * kSortPer;
+constexpr int kSortBinsPer = kSortMaxBins / kSortBlock;
+struct SortPass {
+    Ids ids;                              // the tokens themselves (FIRST),
+    const uint32_t* key_in;               // or sorted pairs
+    const uint32_t* pos_in;
+    int64_t n, rounds;
+    int tiles, shift, bins;               // bins a power of two
+};
+__device__ __forceinline__ uint32_t digit_of(const SortPass& s, uint32_t key) {
+    return (key >> s.shift) & (uint32_t)(s.bins - 1);
 }
-
 // Orders a wave's LDS accesses for the compiler (the hardware keeps them in order).
 __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 }
 
-// Counts the first digit of each tile, and clears the next pass's counts.
-__global__ __launch_bounds__(kSortBlock) void k_count(Ids ids, int64_t n, int64_t tile, Digit d,
-                                                      uint32_t* __restrict__ count,
-                                                      uint32_t* __restrict__ next) {
+// FIRST also notes a token of each row in owner (if there is one to note in).
+template <bool FIRST>
+__global__ __launch_bounds__(kSortBlock) void k_count(SortPass s, uint32_t* __restrict__ count,
+                                                      uint32_t* __restrict__ owner, ClearShape clear) {
+    if (!FIRST && blockIdx.x >= clear.first_block) return clear_block(clear, s.ids, s.n, owner);
     __shared__ uint32_t h[kSortMaxBins];
-    for (int b = threadIdx.x; b < d.bins; b += kSortBlock) h[b] = 0;
+    for (int b = threadIdx.x; b < s.bins; b += kSortBlock) h[b] = 0;
     __syncthreads();
-    const int64_t i1 = (blockIdx.x + 1) * tile < n ? (blockIdx.x + 1) * tile : n;
-    for (int64_t i = blockIdx.x * tile + threadIdx.x; i < i1; i += kSortBlock)
-        atomicAdd(&h[digit_of(d, row_of(ids, i))], 1u);
-    __syncthreads();
-    for (int b = threadIdx.x; b < d.bins; b += kSortBlock) {
-        count[(int64_t)blockIdx.x * d.bins + b] = h[b];
-        next[(int64_t)blockIdx.x * d.bins + b] = 0;
+    for (int64_t r = 0; r < s.rounds; ++r) {
+        const int64_t i0 = (blockIdx.x * s.rounds + r) * kSortTile + threadIdx.x;
+        uint32_t k[kSortPer];
+#pragma unroll
+        for (int u = 0; u < kSortPer; ++u) {
+            const int64_t i = i0 + u * kSortBlock;
+            if (i < s.n) k[u] = FIRST ? row_of(s.ids, i) : s.key_in[i];
+        }
+#pragma unroll
+        for (int u = 0; u < kSortPer; ++u) {
+            const int64_t i = i0 + u * kSortBlock;
+            if (i >= s.n) continue;
+            atomicAdd(&h[digit_of(s, k[u])], 1u);
+            if (FIRST && owner && k[u] != s.ids.rows) owner[k[u]] = (uint32_t)i;
+        }
     }
+    __syncthreads();
+    for (int b = threadIdx.x; b < s.bins; b += kSortBlock) count[(int64_t)blockIdx.x * s.bins + b] = h[b];
 }
 
-// Moves the tokens of one tile to their places by one digit, and counts the next
-// digit (dn.bins > 0) where they land; clears the counts after that.  FIRST reads the
-// tokens themselves, later passes the sorted pairs.  A wave takes a quarter of the
-// tile: it counts its digits, then places them in order from its own bases.
+// Moves the tokens of one tile to their places by one digit.  The block sums the
+// digit counts of all tiles for its bases; in each round wave w counts its kSortPer * 64
+// tokens, then places them in order from its own bases.
 template <bool FIRST>
-__global__ __launch_bounds__(kSortBlock) void k_place(Ids ids, const uint32_t* __restrict__ key_in,
-                                                      const uint32_t* __restrict__ pos_in, int64_t n,
-                                                      int64_t tile, int tiles, Digit d, Digit dn,
-                                                      const uint32_t* __restrict__ count,
-                                                      uint32_t* __restrict__ next,
-                                                      uint32_t* __restrict__ clear,
-                                                      uint32_t* __restrict__ key, uint32_t* __restrict__ pos) {
+__global__ __launch_bounds__(kSortBlock) void k_place(SortPass s, const uint32_t* __restrict__ count,
+                                                      uint32_t* __restrict__ key, uint32_t* __restrict__ pos,
+                                                      const uint32_t* __restrict__ owner, ClearShape clear) {
+    if (blockIdx.x >= clear.first_block) return clear_block(clear, s.ids, s.n, owner);
     __shared__ uint32_t base[kSortWaves][kSortMaxBins];
-    __shared__ uint32_t sums[kSortBlock];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t t0 = blockIdx.x * tile, t1 = t0 + tile < n ? t0 + tile : n;
-    const int64_t quarter = (t1 - t0 + kSortWaves - 1) / kSortWaves;
-    const int64_t w0 = t0 + wave * quarter < t1 ? t0 + wave * quarter : t1;
-    const int64_t w1 = w0 + quarter < t1 ? w0 + quarter : t1;
-    if (clear)
-        for (int b = threadIdx.x; b < d.bins; b += kSortBlock) clear[(int64_t)blockIdx.x * d.bins + b] = 0;
-    for (int b = lane; b < d.bins; b += 64) base[wave][b] = 0;
-    __syncthreads();
-    for (int64_t i = w0 + lane; i < w1; i += 64)
-        atomicAdd(&base[wave][digit_of(d, FIRST ? row_of(ids, i) : key_in[i])], 1u);
-    // Thread t sums the digits [t * per, (t + 1) * per) over all tiles, and those of
-    // the tiles before this one.
-    const int per = (d.bins + kSortBlock - 1) / kSortBlock;
-    uint32_t before[kSortMaxBins / kSortBlock], total[kSortMaxBins / kSortBlock], mine = 0;
+    __shared__ uint32_t next[kSortMaxBins];          // the tile's next place for each digit
+    __shared__ uint32_t sums[kSortWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    // Thread t sums the digits t, t + kSortBlock, ...: over all tiles, and over
+    // those before this one.
+    uint32_t before[kSortBinsPer];
+    uint32_t carry = 0;
 #pragma unroll
-    for (int k = 0; k < kSortMaxBins / kSortBlock; ++k) {
-        const int b = threadIdx.x * per + k;
+    for (int k = 0; k < kSortBinsPer; ++k) {
+        if (k * kSortBlock >= s.bins) continue;
+        const int b = k * kSortBlock + tid;
         uint32_t all = 0, prior = 0;
-        if (k < per && b < d.bins) {
-#pragma unroll 8
-            for (int t = 0; t < tiles; ++t) {
-                const uint32_t c = count[(int64_t)t * d.bins + b];
+        if (b < s.bins) {
+#pragma unroll 16
+            for (int t = 0; t < s.tiles; ++t) {
+                const uint32_t c = count[(int64_t)t * s.bins + b];
                 all += c;
                 prior += t < (int)blockIdx.x ? c : 0;
             }
         }
         before[k] = prior;
-        total[k] = all;
-        mine += all;
-    }
-    sums[threadIdx.x] = mine;
-    __syncthreads();
-    for (int o = 1; o < kSortBlock; o <<= 1) {
-        const uint32_t s = threadIdx.x >= o ? sums[threadIdx.x - o] : 0;
-        __syncthreads();
-        sums[threadIdx.x] += s;
-        __syncthreads();
-    }
-    uint32_t run = sums[threadIdx.x] - mine;
+        uint32_t incl = all;                          // inclusive sum over the wave's digits
 #pragma unroll
-    for (int k = 0; k < kSortMaxBins / kSortBlock; ++k) {
-        const int b = threadIdx.x * per + k;
-        if (k < per && b < d.bins) {
-            uint32_t at = run + before[k];
+        for (int o = 1; o < 64; o <<= 1) {
+            const uint32_t x = __shfl_up(incl, o);
+            incl += lane >= o ? x : 0;
+        }
+        if (lane == 63) sums[wave] = incl;
+        __syncthreads();
+        uint32_t at = carry + incl - all + before[k];
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) {
+            if (w < wave) at += sums[w];
+            carry += sums[w];
+        }
+        if (b < s.bins) next[b] = at;
+        __syncthreads();
+    }
+    for (int64_t r = 0; r < s.rounds; ++r) {
+        // Wave w's tokens: kSortPer times 64 in a row.
+        const int64_t i0 = ((blockIdx.x * s.rounds + r) * kSortWaves + wave) * (64 * kSortPer) + lane;
+        uint32_t k[kSortPer], p[kSortPer];
+#pragma unroll
+        for (int u = 0; u < kSortPer; ++u) {
+            const int64_t i = i0 + 64 * u;
+            k[u] = p[u] = 0;
+            if (i < s.n) {
+                k[u] = FIRST ? row_of(s.ids, i) : s.key_in[i];
+                p[u] = FIRST ? (uint32_t)i : s.pos_in[i];
+            }
+        }
+        for (int b = lane; b < s.bins; b += 64) base[wave][b] = 0;
+        wave_fence();
+#pragma unroll
+        for (int u = 0; u < kSortPer; ++u)
+            if (i0 + 64 * u < s.n) atomicAdd(&base[wave][digit_of(s, k[u])], 1u);
+        __syncthreads();
+        for (int b = tid; b < s.bins; b += kSortBlock) {
+            uint32_t at = next[b];
 #pragma unroll
             for (int w = 0; w < kSortWaves; ++w) {
                 const uint32_t c = base[w][b];
                 base[w][b] = at;
                 at += c;
             }
-            run += total[k];
+            next[b] = at;
         }
-    }
-    __syncthreads();
-    for (int64_t i0 = w0; i0 < w1; i0 += 64) {
-        const int64_t i = i0 + lane;
-        const bool in = i < w1;
-        const uint32_t k = in ? (FIRST ? row_of(ids, i) : key_in[i]) : 0;
-        const uint32_t p = in ? (FIRST ? (uint32_t)i : pos_in[i]) : 0;
-        const uint32_t dg = digit_of(d, k);
-        // The lanes of this wave with the same digit.
-        uint64_t same = __ballot(in);
-        for (int bit = 1; bit < d.bins; bit <<= 1) {
-            const uint64_t m = __ballot((dg & bit) != 0);
-            same &= (dg & bit) ? m : ~m;
-        }
-        const uint32_t rank = __popcll(same & (((uint64_t)1 << lane) - 1));
-        uint32_t at = 0;
-        if (in) at = base[wave][dg] + rank;
-        wave_fence();
-        if (in && rank == 0) base[wave][dg] += __popcll(same);
-        wave_fence();
-        if (in) {
-            key[at] = k;
-            pos[at] = p;
-            if (dn.bins) atomicAdd(&next[(int64_t)(at / (uint32_t)tile) * dn.bins + digit_of(dn, k)], 1u);
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kSortPer; ++u) {
+            const bool in = i0 + 64 * u < s.n;
+            const uint32_t dg = digit_of(s, k[u]);
+            uint64_t same = __ballot(in);             // the lanes with this one's digit
+            for (int bit = 1; bit < s.bins; bit <<= 1) {
+                const uint64_t m = __ballot((dg & bit) != 0);
+                same &= (dg & bit) ? m : ~m;
+            }
+            const uint32_t rank = __popcll(same & (((uint64_t)1 << lane) - 1));
+            uint32_t at = 0;
+            if (in) at = base[wave][dg] + rank;
+            wave_fence();
+            if (in && rank == 0) base[wave][dg] = at + __popcll(same);
+            wave_fence();
+            if (in) { key[at] = k[u]; pos[at] = p[u]; }
         }
     }
 }
@@ -249,210 +376,352 @@ __global__ __launch_bounds__(kSortBlock) void k_place(Ids ids, const uint32_t* _
 //
 // grad[v, c] = (old or 0) + c0 * sum of the kept dy[pos, c] over v's tokens.
 //
-// The sorted tokens are cut into chunks of K; one wave sums the runs of equal
-// rows of one chunk over one tile of columns, in fp32, positions rising.  A run
-// that lies inside its chunk is finished there.  A run over several chunks leaves
-// an fp32 partial sum per chunk: part[2c] where it came from an earlier chunk,
-// part[2c + 1] where it starts in c; k_fold and k_join add them in chunk order.
+// The sorted tokens are cut into chunks of K; one wave sums the runs of equal rows
+// of one chunk over one tile of columns, in fp32, positions rising.  A run that
+// starts in a chunk and ends at most K tokens past it is finished by that chunk's
+// wave (the next chunk's skips it).  A longer run leaves an fp32 partial sum per chunk,
+// part[2c + 1] where it starts in chunk c and part[2c] where it came from an earlier
+// one; k_join adds them in chunk order.
 
 constexpr int kGradBlock = 256, kGradWaves = kGradBlock / 64, kGradCols = 512, kGradUnroll = 8;
-constexpr int kMaxChunk = 64;
+constexpr int kMaxChunk = 32;                         // a wave holds 2 K keys
 
-template <typename G>
-__device__ __forceinline__ void grad_write(G* p, const float sum[8], float c0, bool acc, int64_t left) {
-    float a[8];
+// A lane's columns of a tile of kGradCols, so that the wave's loads of dy are whole
+// lines: 8 in a row for bf16 (16 bytes), two groups of 4 for fp32.
+template <typename T> struct Cols;
+template <> struct Cols<uint16_t> { static constexpr int kPieces = 1, kWidth = 8; };
+template <> struct Cols<float> { static constexpr int kPieces = 2, kWidth = 4; };
+template <typename T>
+__device__ __forceinline__ int64_t piece_col(int p) {
+    return p * 64 * Cols<T>::kWidth + Cols<T>::kWidth * (threadIdx.x & 63);
+}
+
+template <typename T> struct RowPiece;                // a lane's values of one row of dy
+template <> struct RowPiece<uint16_t> { Raw8<uint16_t> r; };
+template <> struct RowPiece<float> { f32x4 a, b; };
+__device__ __forceinline__ f32x4 load4_nt(const float* p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const f32x4_at4*>(p));
+}
+__device__ __forceinline__ f32x4 load4_part(const float* p, int64_t m) {
+    return f32x4{m > 0 ? p[0] : 0.0f, m > 1 ? p[1] : 0.0f, m > 2 ? p[2] : 0.0f, m > 3 ? p[3] : 0.0f};
+}
+// row: the row's values at the tile's first column; left: columns from there on.
+__device__ __forceinline__ RowPiece<uint16_t> load_row(const uint16_t* row, int64_t left) {
+    const int64_t c = piece_col<uint16_t>(0), m = left - c;
+    return {m >= 8 ? load8<true>(row + c) : load8_part(row + c, (int)(m > 0 ? m : 0))};
+}
+__device__ __forceinline__ RowPiece<float> load_row(const float* row, int64_t left) {
+    const int64_t c = piece_col<float>(0), d = piece_col<float>(1);
+    return {left - c >= 4 ? load4_nt(row + c) : load4_part(row + c, left - c),
+            left - d >= 4 ? load4_nt(row + d) : load4_part(row + d, left - d)};
+}
+__device__ __forceinline__ void widen_row(const RowPiece<uint16_t>& r, float a[8]) { widen(r.r, a); }
+__device__ __forceinline__ void widen_row(const RowPiece<float>& r, float a[8]) {
+    widen(Raw8<float>{r.a, r.b}, a);
+}
+// The lane's values zeroed where dropped; first: element index of the tile's first column.
+// Each lane draws the mask of 8 columns in a row; fp32's groups of 4 fetch theirs.
+template <typename T>
+__device__ __forceinline__ uint32_t dropped_row(const DropKey& d, uint64_t first) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t m = dropped8(d, first + 8 * lane);
+    if (Cols<T>::kPieces == 1) return m;
+    const uint32_t lo = (uint32_t)__shfl((int)m, lane >> 1) >> 4 * (lane & 1);
+    const uint32_t hi = (uint32_t)__shfl((int)m, 32 + (lane >> 1)) >> 4 * (lane & 1);
+    return (lo & 15) | (hi & 15) << 4;
+}
+
+// Groups of 4 values of either type (grad and partial rows, at any element).
+__device__ __forceinline__ void load4(const float* p, float a[4]) {
+    const f32x4 x = *reinterpret_cast<const f32x4_at4*>(p);
+    a[0] = x.x; a[1] = x.y; a[2] = x.z; a[3] = x.w;
+}
+__device__ __forceinline__ void load4(const uint16_t* p, float a[4]) {
+    const u32x2 w = *reinterpret_cast<const u32x2_at2*>(p);
+    a[0] = bf16_lo(w.x); a[1] = bf16_hi(w.x); a[2] = bf16_lo(w.y); a[3] = bf16_hi(w.y);
+}
+__device__ __forceinline__ void store4(float* p, const float a[4]) {
+    *reinterpret_cast<f32x4_at4*>(p) = f32x4{a[0], a[1], a[2], a[3]};
+}
+__device__ __forceinline__ void store4(uint16_t* p, const float a[4]) {
+    *reinterpret_cast<u32x2_at2*>(p) = u32x2{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
+}
+// The lane's old values of a row of grad.
+template <typename T, typename G>
+__device__ __forceinline__ void load_old(const G* row, int64_t left, float a[8]) {
+    if (Cols<T>::kPieces == 1 && left - piece_col<T>(0) >= 8) {
+        widen(load8<false>(row + piece_col<T>(0)), a);
+        return;
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a[j] = sum[j] * c0;
-    if (left >= 8) {
-        if (acc) {
-            float b[8];
-            widen(load8<false>(p), b);
+    for (int h = 0; h < 2; ++h) {
+        const int64_t c = Cols<T>::kPieces == 1 ? piece_col<T>(0) + 4 * h : piece_col<T>(h), m = left - c;
+        if (m >= 4) load4(row + c, a + 4 * h);
+        else
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] = b[j] + a[j];
-        }
-        store8<false>(p, a);
-    } else {
-        if (acc) {
-            float b[8];
-            widen(load8_part(p, (int)left), b);
+            for (int j = 0; j < 4; ++j) a[4 * h + j] = j < m ? load1(row + c + j) : 0.0f;
+    }
+}
+template <typename T, typename G>
+__device__ __forceinline__ void store_row(G* row, int64_t left, const float a[8]) {
+    if (Cols<T>::kPieces == 1 && left - piece_col<T>(0) >= 8) {
+        store8<false>(row + piece_col<T>(0), a);
+        return;
+    }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] = b[j] + a[j];
-        }
-        store8_part(p, a, (int)left);
+    for (int h = 0; h < 2; ++h) {
+        const int64_t c = Cols<T>::kPieces == 1 ? piece_col<T>(0) + 4 * h : piece_col<T>(h), m = left - c;
+        if (m >= 4) store4(row + c, a + 4 * h);
+        else
+#pragma unroll
+            for (int j = 0; j < 4; ++j) if (j < m) store1(row + c + j, a[4 * h + j]);
     }
 }
 
-// Partial rows are padded to whole vectors.
-__device__ __forceinline__ void part_write(float* p, const float sum[8], int64_t left) {
-    if (left > 0) store8<false>(p, sum);
-}
-
 struct GradShape {
-    int64_t dim, pitch;                  // pitch: floats of a partial row
+    int64_t dim, pitch;                  // pitch: floats of a partial row, a multiple of 8
     int64_t n, chunks;
     uint32_t rows;
-    int K, col_blocks, acc;
-    int64_t sum_blocks;                  // blocks that sum; the rest clear rows
-    int clear_rows;                      // rows per clearing block
+    int K, tiles;                        // tiles of columns
 };
 
-template <typename T, typename G, bool DROP>
+template <typename T, typename G, bool ACC, bool DROP>
 __global__ __launch_bounds__(kGradBlock) void k_grad(const T* __restrict__ dy, const uint32_t* __restrict__ key,
                                                      const uint32_t* __restrict__ pos, GradShape s,
                                                      float c0, DropArgs da, G* __restrict__ grad,
                                                      float* __restrict__ part) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if ((int64_t)blockIdx.x >= s.sum_blocks) {
-        // Clears the rows without a token among clear_rows of them.
-        const int64_t r0 = ((int64_t)blockIdx.x - s.sum_blocks) * s.clear_rows;
-        const int64_t v = r0 + lane;
-        bool missing = lane < s.clear_rows && v < (int64_t)s.rows;
-        if (missing) {
-            int64_t lo = 0, hi = s.n;    // the first sorted place with key >= v
-            while (lo < hi) {
-                const int64_t mid = (lo + hi) >> 1;
-                if (key[mid] < (uint32_t)v) lo = mid + 1; else hi = mid;
-            }
-            missing = lo >= s.n || key[lo] != (uint32_t)v;
-        }
-        const float zero[8] = {};
-        for (uint64_t m = __ballot(missing); m; m &= m - 1) {
-            G* p = grad + (r0 + __builtin_ctzll(m)) * s.dim;
-            for (int64_t c = 8 * (int64_t)threadIdx.x; c < s.dim; c += 8 * kGradBlock) {
-                if (s.dim - c >= 8) store8<true>(p + c, zero);
-                else store8_part(p + c, zero, (int)(s.dim - c));
-            }
-        }
-        return;
+    const int lane = threadIdx.x & 63;
+    const int64_t w = (int64_t)blockIdx.x * kGradWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t chunk = w / s.tiles;
+    if (chunk >= s.chunks) return;
+    const int64_t c = (w - chunk * s.tiles) * kGradCols, left = s.dim - c;
+    const int64_t s0 = chunk * s.K, s1 = s0 + s.K;
+    // Lane l holds the key and position of token s0 + l, l < 2 K.
+    uint32_t my_key = s.rows, my_pos = 0;
+    if (lane < 2 * s.K && s0 + lane < s.n) { my_key = key[s0 + lane]; my_pos = pos[s0 + lane]; }
+    const uint32_t none = 0xFFFFFFFFu;                               // no row's number
+    const uint32_t before = s0 > 0 ? key[s0 - 1] : none, long_before = s0 > s.K ? key[s0 - s.K - 1] : none;
+    const uint32_t after = s1 + s.K < s.n ? key[s1 + s.K] : none;
+    const uint32_t k_first = __builtin_amdgcn_readlane(my_key, 0), k_last = __builtin_amdgcn_readlane(my_key, s.K - 1);
+    const uint32_t k_next = __builtin_amdgcn_readlane(my_key, s.K), k_past = after;
+    int first = 0, last = __popcll(__ballot(lane < s.K && my_key != s.rows));
+    bool head_part = false, tail_part = false;
+    if (k_first == before) {                                         // a run goes on from the last chunk
+        if (long_before != k_first && k_next != k_first)             // that chunk finishes it
+            first = __popcll(__ballot(lane < s.K && my_key == k_first));
+        else head_part = true;
     }
-    const int64_t chunk = (int64_t)blockIdx.x / s.col_blocks;
-    const int64_t c_tile = ((int64_t)(blockIdx.x % s.col_blocks) * kGradWaves + wave) * kGradCols;
-    if (c_tile >= s.dim) return;
-    // Lanes past the last column stay: every lane holds a key.
-    const int64_t c = c_tile + 8 * lane, left = s.dim - c > 0 ? s.dim - c : 0;
+    if (k_last == k_next && s.K == last) {                           // a run goes on into the next
+        if (k_last != before && k_past != k_last) last += __popcll(__ballot(lane >= s.K && my_key == k_last));
+        else tail_part = k_last != before;
+    }
+    if (first >= last) return;
     DropKey d{};
     if (DROP) d = drop_key(da);
-    const int64_t s0 = chunk * s.K;
-    const int m = (int)(s.n - s0 < s.K ? s.n - s0 : s.K);
-    // lane l holds the chunk's l-th key and position
-    const uint32_t my_key = lane < m ? key[s0 + lane] : s.rows, my_pos = lane < m ? pos[s0 + lane] : 0;
-    const uint32_t prev = s0 > 0 ? key[s0 - 1] : s.rows, next = s0 + m < s.n ? key[s0 + m] : s.rows;
-    uint32_t cur = __builtin_amdgcn_readfirstlane(my_key);
-    if (cur == s.rows) return;                        // from here on no token has a row
-    bool from_before = cur == prev;
     float sum[8] = {};
-    for (int k0 = 0; k0 < m; k0 += kGradUnroll) {
-        Raw8<T> r[kGradUnroll];
+    for (int t = first; t < last; t += kGradUnroll) {
+        RowPiece<T> r[kGradUnroll];
+        float old[ACC ? kGradUnroll : 1][8];
         uint32_t kk[kGradUnroll], pp[kGradUnroll];
+        bool ends[kGradUnroll];
 #pragma unroll
         for (int u = 0; u < kGradUnroll; ++u) {
-            const int at = k0 + u < m ? k0 + u : m - 1;
+            const int at = t + u < last ? t + u : last - 1;
             kk[u] = __builtin_amdgcn_readlane(my_key, at);
             pp[u] = __builtin_amdgcn_readlane(my_pos, at);
-            if (k0 + u >= m) kk[u] = s.rows;
-            const T* p = dy + (int64_t)pp[u] * s.dim + c;
-            r[u] = left >= 8 ? load8<true>(p) : load8_part(p, (int)left);
+            ends[u] = at + 1 == last || (uint32_t)__builtin_amdgcn_readlane(my_key, at + 1) != kk[u];
+            if (t + u < last) r[u] = load_row(dy + (int64_t)pp[u] * s.dim + c, left);
+            if (ACC && t + u < last && ends[u]) load_old<T>(grad + (int64_t)kk[u] * s.dim + c, left, old[u]);
+        }
+        uint32_t gone[2] = {};                                       // 8 bits for each u
+        if (DROP) {
+#pragma unroll 1
+            for (int u = 0; u < kGradUnroll && t + u < last; ++u) {
+                const uint32_t p = __builtin_amdgcn_readlane(my_pos, t + u);
+                const uint32_t m = dropped_row<T>(d, (uint64_t)p * (uint64_t)s.dim + (uint64_t)c) << 8 * (u & 3);
+                gone[0] |= u < 4 ? m : 0;
+                gone[1] |= u < 4 ? 0 : m;
+            }
         }
 #pragma unroll
         for (int u = 0; u < kGradUnroll; ++u) {
-            if (kk[u] != cur) {
-                if (cur != s.rows) {
-                    if (from_before) part_write(part + 2 * chunk * s.pitch + c, sum, left);
-                    else grad_write(grad + (int64_t)cur * s.dim + c, sum, c0, s.acc != 0, left);
+            if (t + u >= last) break;
+            float a[8];
+            widen_row(r[u], a);
+            if (DROP) drop8(gone[u >> 2] >> 8 * (u & 3), a);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] = sum[j] + a[j];
+            if (!ends[u]) continue;
+            if (head_part || (tail_part && t + u + 1 == last)) {
+                store_row<T>(part + (2 * chunk + (head_part ? 0 : 1)) * s.pitch + c, s.pitch - c, sum);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    a[j] = sum[j] * c0;
+                    if (ACC) a[j] = old[ACC ? u : 0][j] + a[j];
                 }
-                from_before = false;
-                cur = kk[u];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+                store_row<T>(grad + (int64_t)kk[u] * s.dim + c, left, a);
             }
-            if (kk[u] != s.rows) {
-                float a[8];
-                widen(r[u], a);
-                if (DROP) drop8(d, (uint64_t)pp[u] * (uint64_t)s.dim + (uint64_t)c, a);
+            head_part = false;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum[j] = sum[j] + a[j];
-            }
+            for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
         }
     }
-    if (cur == s.rows) return;
-    if (from_before) part_write(part + 2 * chunk * s.pitch + c, sum, left);
-    else if (cur == next) part_write(part + (2 * chunk + 1) * s.pitch + c, sum, left);
-    else grad_write(grad + (int64_t)cur * s.dim + c, sum, c0, s.acc != 0, left);
 }
 
-// Partial sums of one run are folded kFold at a time: where the aligned group of
-// kFold chunks of `step` chunks each lies inside one run, past its first chunk, their
-// sum takes the place of the group's first partial.
-constexpr int kFold = 32, kJoinCols = 256;
-__device__ __forceinline__ bool inside_run(const uint32_t* __restrict__ key, const GradShape& s,
-                                           int64_t c, int64_t len) {
-    // every token of the chunks [c, c + len) has the row of the token before them
-    if (c + len > s.chunks || c == 0) return false;
-    const int64_t last = (c + len) * s.K - 1 < s.n ? (c + len) * s.K - 1 : s.n - 1;
-    const uint32_t k = key[c * s.K - 1];
-    return k != s.rows && key[last] == k;
-}
-__device__ __forceinline__ f32x4 sum_rows(const float* __restrict__ p, int64_t pitch, int count, f32x4 a) {
-    int k = 0;
-    for (; k + 8 <= count; k += 8) {
+// Finishes the runs that k_grad left in parts.  A block looks at 64 chunks and takes
+// kJoinCols columns of the runs that start in one of them and leave a tail part: a run
+// of at most kJoinWaves parts is one wave's, a longer one the block's, each wave
+// summing a stretch of its parts and the first wave those sums, all in order.
+constexpr int kJoinBlock = 1024, kJoinWaves = kJoinBlock / 64, kJoinCols = 256;
+// a + part rows [k, end) of the run that starts in `chunk`, at the lane's columns.
+__device__ __forceinline__ f32x4 sum_parts(const float* __restrict__ part, int64_t pitch, int64_t chunk,
+                                           int64_t k, int64_t end) {
+    f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto row = [&](int64_t i) { return ldf4(part + (2 * (chunk + i) + (i == 0)) * pitch); };
+    for (; k + 8 <= end; k += 8) {
         f32x4 x[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) x[u] = ldf4(p + (k + u) * pitch);
+        for (int u = 0; u < 8; ++u) x[u] = row(k + u);
 #pragma unroll
         for (int u = 0; u < 8; ++u) a = add4(a, x[u]);
     }
-    for (; k < count; ++k) a = add4(a, ldf4(p + k * pitch));
+    for (; k < end; ++k) a = add4(a, row(k));
     return a;
 }
-__global__ __launch_bounds__(kGradBlock) void k_fold(const uint32_t* __restrict__ key, GradShape s,
-                                                     int64_t step, float* __restrict__ part) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c0 = (int64_t)(blockIdx.x / s.col_blocks) * kFold * step;
-    const int64_t c = ((int64_t)(blockIdx.x % s.col_blocks) * kGradWaves + wave) * kJoinCols + 4 * lane;
-    if (c >= s.pitch || !inside_run(key, s, c0, kFold * step)) return;
-    float* p = part + 2 * c0 * s.pitch + c;
-    stf4(p, sum_rows(p + 2 * step * s.pitch, 2 * step * s.pitch, kFold - 1, ldf4(p)));
+template <typename G, bool ACC>
+__global__ __launch_bounds__(kJoinBlock) void k_join(const uint32_t* __restrict__ key, GradShape s, int tiles,
+                                                     float c0, G* __restrict__ grad,
+                                                     const float* __restrict__ part) {
+    __shared__ f32x4 sums[kJoinWaves][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t g = (int64_t)blockIdx.x / tiles, c0l = ((int64_t)blockIdx.x % tiles) * kJoinCols;
+    const int64_t c = c0l + 4 * lane, cp = c < s.pitch ? c : 0;        // lanes past the row read its start
+    const int64_t mine = g * 64 + lane, e = (mine + 1) * s.K;        // this lane's chunk and its end
+    uint32_t k = s.rows;
+    bool starts = false;
+    if (mine < s.chunks && e < s.n) {
+        k = key[e - 1];
+        const uint32_t next = key[e], before = mine > 0 ? key[e - s.K - 1] : 0xFFFFFFFFu;
+        const uint32_t past = e + s.K < s.n ? key[e + s.K] : 0xFFFFFFFFu;
+        starts = k != s.rows && k == next && k != before && k == past;
+    }
+    int order = 0;
+    for (uint64_t m = __ballot(starts); m; m &= m - 1, ++order) {
+        const int l = __builtin_ctzll(m);
+        const uint32_t row = __builtin_amdgcn_readlane(k, l);
+        const int64_t chunk = g * 64 + l;
+        int64_t parts = 1;                                           // with the chunks that the run goes on into
+        for (;;) {
+            const int64_t j = chunk + parts + lane;
+            const uint64_t on = __ballot(j < s.chunks && key[j < s.chunks ? j * s.K : 0] == row);
+            const int more = ~on ? __builtin_ctzll(~on) : 64;
+            parts += more;
+            if (more < 64) break;
+        }
+        f32x4 a;
+        if (parts <= kJoinWaves) {
+            if (order % kJoinWaves != wave) continue;
+            a = sum_parts(part + cp, s.pitch, chunk, 0, parts);
+        } else {
+            sums[wave][lane] = sum_parts(part + cp, s.pitch, chunk, parts * wave / kJoinWaves, parts * (wave + 1) / kJoinWaves);
+            __syncthreads();
+            if (wave == 0) {
+                a = sums[0][lane];
+                for (int w = 1; w < kJoinWaves; ++w) a = add4(a, sums[w][lane]);
+            }
+            __syncthreads();
+            if (wave != 0) continue;
+        }
+        float v[4] = {a.x * c0, a.y * c0, a.z * c0, a.w * c0};
+        G* p = grad + (int64_t)row * s.dim + c;
+        const int64_t left = s.dim - c;
+        if (left >= 4) {
+            if (ACC) {
+                float o[4];
+                load4(p, o);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = o[j] + v[j];
+            }
+            store4(p, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < left) store1(p + j, ACC ? load1(p + j) + v[j] : v[j]);
+        }
+    }
 }
 
-// Finishes the runs that start in a chunk and go on past it: the sum of the
-// chunk's last partial and of the following chunks' first ones, folded groups
-// taken whole.
-template <typename G>
-__global__ __launch_bounds__(kGradBlock) void k_join(const uint32_t* __restrict__ key, GradShape s,
-                                                     int64_t max_step, float c0, G* __restrict__ grad,
-                                                     const float* __restrict__ part) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t chunk = (int64_t)blockIdx.x / s.col_blocks;
-    const int64_t c = ((int64_t)(blockIdx.x % s.col_blocks) * kGradWaves + wave) * kJoinCols + 4 * lane;
-    if (c >= s.pitch || chunk + 1 >= s.chunks) return;
-    const int64_t s1 = (chunk + 1) * s.K;
-    const uint32_t k = key[s1 - 1];
-    if (k == s.rows || key[s1] != k) return;                         // ends with its chunk
-    if (chunk > 0 && key[chunk * s.K - 1] == k) return;              // started earlier
-    int64_t lo = s1, hi = s.n;                                       // the first place past the run
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (key[mid] == k) lo = mid + 1; else hi = mid;
+// ---------------------------------------------------- a few tokens at once --
+
+// n <= kDirectMax tokens in one launch without a sort: the wave of (token, tile of
+// columns) ends if its row came earlier, else it sums the tokens of its row in order.
+// Blocks from clear.first_block on clear the rows that no token has.
+constexpr int kDirectMax = 128;
+template <typename T, typename G, bool ACC, bool DROP>
+__global__ __launch_bounds__(kGradBlock) void k_direct(const T* __restrict__ dy, Ids ids, GradShape s, float c0,
+                                                       DropArgs da, G* __restrict__ grad, ClearShape clear) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t k0 = lane < s.n ? row_of(ids, lane) : s.rows, k1 = lane + 64 < s.n ? row_of(ids, lane + 64) : s.rows;
+    if (!ACC && blockIdx.x >= clear.first_block) {
+        const int64_t r0 = (int64_t)(blockIdx.x - clear.first_block) * clear.per, v = r0 + lane;
+        bool missing = lane < clear.per && v < clear.row1;
+        for (int j = 0; j < 64; ++j) {
+            if ((uint32_t)__builtin_amdgcn_readlane(k0, j) == (uint64_t)v) missing = false;
+            if ((uint32_t)__builtin_amdgcn_readlane(k1, j) == (uint64_t)v) missing = false;
+        }
+        clear_rows(grad, s.dim, r0, __ballot(missing));
+        return;
     }
-    // The run holds the first tokens of chunks [chunk + 1, end) and all of [chunk + 1, whole).
-    const int64_t end = (lo + s.K - 1) / s.K, whole = lo == s.n ? s.chunks : lo / s.K;
-    f32x4 a = ldf4(part + (2 * chunk + 1) * s.pitch + c);
-    for (int64_t at = chunk + 1; at < end;) {
-        int64_t step = max_step;                                     // the largest folded group at `at`
-        while (step > 1 && (at % step != 0 || at + step > whole)) step /= kFold;
-        int64_t limit = step > 1 ? whole : end;                      // equal steps up to the next larger group
-        if (step < max_step && limit > (at / (step * kFold) + 1) * (step * kFold))
-            limit = (at / (step * kFold) + 1) * (step * kFold);
-        const int64_t count = (limit - at) / step;
-        a = sum_rows(part + 2 * at * s.pitch + c, 2 * step * s.pitch, (int)count, a);
-        at += count * step;
-    }
-    const int64_t left = s.dim - c;
-    G* p = grad + (int64_t)k * s.dim + c;
-    const float v[4] = {a.x * c0, a.y * c0, a.z * c0, a.w * c0};
+    const int64_t w = (int64_t)blockIdx.x * kGradWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int i = (int)(w / s.tiles);
+    if (i >= s.n) return;
+    const int64_t c = (w - (int64_t)i * s.tiles) * kGradCols, left = s.dim - c;
+    const uint32_t mine = i < 64 ? __builtin_amdgcn_readlane(k0, i) : __builtin_amdgcn_readlane(k1, i - 64);
+    uint64_t m0 = __ballot(k0 == mine), m1 = __ballot(k1 == mine);
+    if (mine == s.rows || (m0 ? __builtin_ctzll(m0) : 64 + __builtin_ctzll(m1)) != i) return;
+    DropKey d{};
+    if (DROP) d = drop_key(da);
+    float sum[8] = {}, old[8];
+    if (ACC) load_old<T>(grad + (int64_t)mine * s.dim + c, left, old);
+    while (m0 | m1) {
+        uint64_t n0 = m0, n1 = m1;                    // the same tokens once more, for their masks
+        RowPiece<T> r[kGradUnroll];
+        int at[kGradUnroll];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (j < left) store1(p + j, s.acc ? load1(p + j) + v[j] : v[j]);
+        for (int u = 0; u < kGradUnroll; ++u) {
+            at[u] = -1;
+            if (m0) { at[u] = __builtin_ctzll(m0); m0 &= m0 - 1; }
+            else if (m1) { at[u] = 64 + __builtin_ctzll(m1); m1 &= m1 - 1; }
+            if (at[u] >= 0) r[u] = load_row(dy + (int64_t)at[u] * s.dim + c, left);
+        }
+        uint32_t gone[2] = {};
+        if (DROP) {
+#pragma unroll 1
+            for (int u = 0; u < kGradUnroll && (n0 | n1); ++u) {
+                const int p = n0 ? __builtin_ctzll(n0) : 64 + __builtin_ctzll(n1);
+                if (n0) n0 &= n0 - 1; else n1 &= n1 - 1;
+                const uint32_t m = dropped_row<T>(d, (uint64_t)p * (uint64_t)s.dim + (uint64_t)c) << 8 * (u & 3);
+                gone[0] |= u < 4 ? m : 0;
+                gone[1] |= u < 4 ? 0 : m;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kGradUnroll; ++u) {
+            if (at[u] < 0) break;
+            float a[8];
+            widen_row(r[u], a);
+            if (DROP) drop8(gone[u >> 2] >> 8 * (u & 3), a);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] = sum[j] + a[j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        sum[j] = sum[j] * c0;
+        if (ACC) sum[j] = old[j] + sum[j];
+    }
+    store_row<T>(grad + (int64_t)mine * s.dim + c, left, sum);
 }
 
 }  // namespace

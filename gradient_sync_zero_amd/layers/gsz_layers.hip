@@ -90,16 +90,14 @@ int grid_for(int64_t tiles, int block) {
 
 // ------------------------------------------------------- gradient's plan --
 
-struct SortShape { bool rank; int64_t tile; int tiles, bits, passes; };
-
+// The counting sort of n > kRankMax tokens: at most 256 tiles (every block of a pass
+// reads the digit counts of all of them) and digits of at most 10 bits.
+struct SortShape { int64_t rounds; int tiles, bits, passes; };
 SortShape sort_shape(int64_t n, int64_t rows) {
     SortShape s{};
-    s.rank = n <= kRankMax;
-    if (s.rank) return s;
-    // At most 256 tiles: every block of a pass reads the digit counts of all of them.
-    s.tile = 1024;
-    while ((n + s.tile - 1) / s.tile > 256) s.tile *= 2;
-    s.tiles = (int)((n + s.tile - 1) / s.tile);
+    s.rounds = 1;
+    while ((n + s.rounds * kSortTile - 1) / (s.rounds * kSortTile) > 256) s.rounds *= 2;
+    s.tiles = (int)((n + s.rounds * kSortTile - 1) / (s.rounds * kSortTile));
     int bits = 1;
     while (((int64_t)1 << bits) <= rows) ++bits;          // keys [0, rows]
     s.passes = (bits + 9) / 10;
@@ -107,25 +105,29 @@ SortShape sort_shape(int64_t n, int64_t rows) {
     return s;
 }
 
+int col_tiles(int64_t dim) { return (int)((dim + kGradCols - 1) / kGradCols); }
+
 int chunk_for(int64_t n, int64_t dim) {
-    const int64_t cols = (dim + kGradCols - 1) / kGradCols;
     int K = kMaxChunk;
-    while (K > 8 && (n + K - 1) / K * cols < 4096) K /= 2;
+    while (K > 8 && (n + K - 1) / K * col_tiles(dim) < 4096) K /= 2;
     return K;
 }
 
-struct Workspace { size_t key[2], pos[2], count[3], part, bytes; };
-
+struct Workspace { size_t key[2], pos[2], count, owner, part, bytes; };
 Workspace workspace_for(int64_t n, int64_t rows, int64_t dim) {
     Workspace w{};
+    if (n <= kDirectMax) return w;
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t o = at; at += (bytes + 255) / 256 * 256; return o; };
-    const SortShape s = sort_shape(n, rows);
-    for (int k = 0; k < (s.rank ? 1 : 2); ++k) { w.key[k] = take(4 * n); w.pos[k] = take(4 * n); }
-    if (!s.rank)
-        for (int k = 0; k < 3; ++k) w.count[k] = take((size_t)4 * s.tiles << s.bits);
-    const int64_t chunks = (n + chunk_for(n, dim) - 1) / chunk_for(n, dim), pitch = (dim + 7) / 8 * 8;
-    w.part = take((size_t)8 * chunks * pitch);
+    const bool rank = n <= kRankMax;
+    for (int k = 0; k < (rank ? 1 : 2); ++k) { w.key[k] = take(4 * n); w.pos[k] = take(4 * n); }
+    if (!rank) {
+        const SortShape s = sort_shape(n, rows);
+        w.count = take((size_t)4 * s.tiles << s.bits);
+        w.owner = take((size_t)4 * rows);
+    }
+    const int64_t chunks = (n + chunk_for(n, dim) - 1) / chunk_for(n, dim);
+    w.part = take((size_t)8 * chunks * ((dim + 7) / 8 * 8));
     w.bytes = at;
     return w;
 }
@@ -189,10 +191,19 @@ extern "C" int gsz_embedding_lookup(const void* table, int32_t table_type, int64
     if (off_by(table, ts) || off_by(out, os) || off_by(ids, is)) { set_error("%s: a buffer is not aligned to its values", who); return GSZ_ERR_MISALIGNED; }
     if ((rc = check_device(who))) return rc;
     if (!work) return GSZ_OK;
-    const int64_t vpr = (dim + 7) / 8;
-    const int tile_rows = vpr >= kLookVecs ? 1 : (int)(kLookVecs / vpr);
-    const uint64_t magic = ((uint64_t)1 << 32) / (uint64_t)vpr + 1;
-    const int grid = grid_for((n + tile_rows - 1) / tile_rows, kLookBlock);
+    LookShape l{};
+    l.n = n;
+    l.dim = dim;
+    l.vpr = (dim + 7) / 8;
+    l.slices = 8;
+    while (l.slices > 1 && l.vpr / l.slices < 64) l.slices /= 2;      // a wave's load stays in one row
+    l.sv = (l.vpr + l.slices - 1) / l.slices;
+    int64_t vecs = kLookVecs;                                         // per block
+    while (vecs > kLookBlock && n * l.vpr / vecs < 2048) vecs /= 2;
+    l.tile_rows = l.sv >= vecs ? 1 : (int)(vecs / l.sv);
+    l.magic = ((uint64_t)1 << 32) / (uint64_t)l.sv + 1;
+    l.tiles = (n + l.tile_rows - 1) / l.tile_rows;
+    const int grid = grid_for(l.tiles * l.slices, kLookBlock);
     const Ids id{ids, id_type == GSZ_TYPE_I64, (uint32_t)rows};
     with_type(table_type, [&](auto t) {
         with_type(out_type, [&](auto o) {
@@ -200,8 +211,7 @@ extern "C" int gsz_embedding_lookup(const void* table, int32_t table_type, int64
                 using T = decltype(t);
                 using O = decltype(o);
                 hipLaunchKernelGGL((k_lookup<T, O, decltype(drop)::value>), dim3(grid), dim3(kLookBlock), 0,
-                                   stream, static_cast<const T*>(table), id, n, dim, vpr, tile_rows, magic, c0,
-                                   da, static_cast<O*>(out));
+                                   stream, static_cast<const T*>(table), id, l, c0, da, static_cast<O*>(out));
             });
         });
     });
@@ -231,8 +241,8 @@ extern "C" int gsz_embedding_grad(const void* ids, int32_t id_type, int64_t n, c
     float c0;
     if ((rc = check_drop(who, p, scale, rng, site, &da, &c0))) return rc;
     const Workspace w = workspace_for(n, rows, dim);
-    if (n > 0 && dim > 0) {
-        if (!ids || !dy) return bad_arg(who, "NULL buffer");
+    if (n > 0 && dim > 0 && (!ids || !dy)) return bad_arg(who, "NULL buffer");
+    if (n > 0 && dim > 0 && w.bytes > 0) {
         if (!ws || ws_bytes < w.bytes) { set_error("%s: workspace of %zu bytes required", who, w.bytes); return GSZ_ERR_SIZE; }
         if (off_by(ws, 16)) { set_error("%s: workspace is not 16-byte aligned", who); return GSZ_ERR_MISALIGNED; }
     }
@@ -247,16 +257,20 @@ extern "C" int gsz_embedding_grad(const void* ids, int32_t id_type, int64_t n, c
     g.rows = (uint32_t)rows;
     g.K = chunk_for(n, dim);
     g.chunks = (n + g.K - 1) / g.K;
-    g.col_blocks = (int)((dim + kGradCols * kGradWaves - 1) / (kGradCols * kGradWaves));
-    g.acc = accumulate;
-    g.sum_blocks = g.chunks * g.col_blocks;
-    // A clearing block writes about 128 KiB.
-    const int64_t want = ((int64_t)128 << 10) / (dim * gs);
-    g.clear_rows = (int)(want < 1 ? 1 : want > 64 ? 64 : want);
-    const int64_t blocks = g.sum_blocks + (accumulate ? 0 : (rows + g.clear_rows - 1) / g.clear_rows);
-    GradShape j = g;
-    j.col_blocks = (int)((g.pitch + kJoinCols * kGradWaves - 1) / (kJoinCols * kGradWaves));
-    if (blocks > kMaxWorkItems / kGradBlock || g.chunks * j.col_blocks > kMaxWorkItems / kGradBlock) {
+    g.tiles = col_tiles(dim);
+    const bool direct = n <= kDirectMax, rank = !direct && n <= kRankMax, f32 = grad_type == GSZ_TYPE_F32;
+    // Rows that a block clears: about 128 KiB beside the sort's or the sums' blocks,
+    // 256 KiB in whole words of 64 rows for the rank sort's, which hold every key.
+    const int64_t row_bytes = dim * gs;
+    auto clamp = [](int64_t v, int64_t most) { return (int)(v < 1 ? 1 : v > most ? most : v); };
+    const int per = rank ? clamp(((int64_t)256 << 10) / (64 * row_bytes), 64) : clamp(((int64_t)128 << 10) / row_bytes, 64);
+    const int64_t clear_blocks = accumulate ? 0 : (rows + (int64_t)per * (rank ? 64 : 1) - 1) / ((int64_t)per * (rank ? 64 : 1));
+    const int64_t sum_blocks = ((direct ? n : g.chunks) * g.tiles + kGradWaves - 1) / kGradWaves;
+    const int join_tiles = (int)((dim + kJoinCols - 1) / kJoinCols);
+    const int64_t join_blocks = (g.chunks + 63) / 64 * join_tiles;
+    const int64_t rank_blocks = (n + kRankTokens - 1) / kRankTokens > clear_blocks ? (n + kRankTokens - 1) / kRankTokens : clear_blocks;
+    if (sum_blocks + (rank ? 0 : clear_blocks) + 256 > kMaxWorkItems / kGradBlock ||
+        join_blocks > kMaxWorkItems / kJoinBlock || (rank && rank_blocks > kMaxWorkItems / kRankBlock)) {
         set_error("%s: n %lld by dim %lld, or rows %lld, needs more than 2^31 work-items", who, (long long)n, (long long)dim, (long long)rows);
         return GSZ_ERR_SIZE;
     }
@@ -265,60 +279,93 @@ extern "C" int gsz_embedding_grad(const void* ids, int32_t id_type, int64_t n, c
     char* base = static_cast<char*>(ws);
     auto u32 = [&](size_t o) { return reinterpret_cast<uint32_t*>(base + o); };
     const Ids id{ids, id_type == GSZ_TYPE_I64, (uint32_t)rows};
-    const uint32_t* key = nullptr;
-    const uint32_t* pos = nullptr;
-    if (n > 0) {
-        const SortShape s = sort_shape(n, rows);
-        if (s.rank) {
-            hipLaunchKernelGGL(k_rank, dim3((unsigned)((n + 63) / 64)), dim3(kRankBlock), 0, stream, id, (int)n,
-                               u32(w.key[0]), u32(w.pos[0]));
-            if ((rc = launched(who))) return rc;
-            key = u32(w.key[0]);
-            pos = u32(w.pos[0]);
-        } else {
-            const int bins = 1 << s.bits;
-            hipLaunchKernelGGL(k_count, dim3(s.tiles), dim3(kSortBlock), 0, stream, id, n, s.tile, Digit{0, bins},
-                               u32(w.count[0]), u32(w.count[1]));
-            if ((rc = launched(who))) return rc;
-            for (int k = 0; k < s.passes; ++k) {
-                const Digit d{k * s.bits, bins}, dn{(k + 1) * s.bits, k + 1 < s.passes ? bins : 0};
-                uint32_t* clear = k + 2 < s.passes ? u32(w.count[(k + 2) % 3]) : nullptr;
-                uint32_t* to_key = u32(w.key[k & 1]);
-                uint32_t* to_pos = u32(w.pos[k & 1]);
-                with_bool(k == 0, [&](auto first) {
-                    hipLaunchKernelGGL((k_place<decltype(first)::value>), dim3(s.tiles), dim3(kSortBlock), 0, stream,
-                                       id, key, pos, n, s.tile, s.tiles, d, dn, u32(w.count[k % 3]),
-                                       u32(w.count[(k + 1) % 3]), clear, to_key, to_pos);
+    ClearShape clear{accumulate ? nullptr : grad, dim, 0, rows, 0xFFFFFFFFu, per, f32};
+    if (direct) {
+        clear.first_block = (unsigned)sum_blocks;
+        with_type(dy_type, [&](auto t) {
+            with_type(grad_type, [&](auto o) {
+                with_bool(accumulate != 0, [&](auto acc) {
+                    with_bool(da.threshold != 0, [&](auto drop) {
+                        using T = decltype(t);
+                        using G = decltype(o);
+                        hipLaunchKernelGGL((k_direct<T, G, decltype(acc)::value, decltype(drop)::value>),
+                                           dim3((unsigned)(sum_blocks + clear_blocks)), dim3(kGradBlock), 0, stream,
+                                           static_cast<const T*>(dy), id, g, c0, da, static_cast<G*>(grad), clear);
+                    });
                 });
+            });
+        });
+        return launched(who);
+    }
+
+    uint32_t* key = u32(w.key[0]);
+    uint32_t* pos = u32(w.pos[0]);
+    if (rank) {
+        with_bool(rows < kRankPackedRows, [&](auto packed) {
+            hipLaunchKernelGGL((k_rank<decltype(packed)::value>), dim3((unsigned)rank_blocks), dim3(kRankBlock), 0,
+                               stream, id, (int)n, key, pos, clear);
+        });
+        if ((rc = launched(who))) return rc;
+    } else {
+        const SortShape sh = sort_shape(n, rows);
+        SortPass s{id, nullptr, nullptr, n, sh.rounds, sh.tiles, 0, 1 << sh.bits};
+        uint32_t* count = u32(w.count);
+        uint32_t* owner = accumulate ? nullptr : u32(w.owner);
+        // The launches after the first each clear a part of the rows.
+        const int parts = 2 * sh.passes - 1;
+        int part = 0;
+        auto next_part = [&]() -> int64_t {                          // its blocks
+            clear.first_block = accumulate ? 0xFFFFFFFFu : (unsigned)sh.tiles;
+            clear.row0 = clear_blocks * part / parts * per;
+            clear.row1 = ++part == parts ? rows : clear_blocks * part / parts * per;
+            return accumulate ? 0 : (clear.row1 - clear.row0 + per - 1) / per;
+        };
+        for (int k = 0; k < sh.passes; ++k) {
+            s.shift = k * sh.bits;
+            key = u32(w.key[k & 1]);
+            pos = u32(w.pos[k & 1]);
+            if (k == 0) {
+                hipLaunchKernelGGL((k_count<true>), dim3(sh.tiles), dim3(kSortBlock), 0, stream, s, count, owner, clear);
                 if ((rc = launched(who))) return rc;
-                key = to_key;
-                pos = to_pos;
+                const int64_t more = next_part();
+                hipLaunchKernelGGL((k_place<true>), dim3((unsigned)(sh.tiles + more)), dim3(kSortBlock), 0, stream, s,
+                                   count, key, pos, owner, clear);
+            } else {
+                int64_t more = next_part();
+                hipLaunchKernelGGL((k_count<false>), dim3((unsigned)(sh.tiles + more)), dim3(kSortBlock), 0, stream, s,
+                                   count, owner, clear);
+                if ((rc = launched(who))) return rc;
+                more = next_part();
+                hipLaunchKernelGGL((k_place<false>), dim3((unsigned)(sh.tiles + more)), dim3(kSortBlock), 0, stream, s,
+                                   count, key, pos, owner, clear);
             }
+            if ((rc = launched(who))) return rc;
+            s.key_in = key;
+            s.pos_in = pos;
         }
     }
+
     float* part = reinterpret_cast<float*>(base + w.part);
     with_type(dy_type, [&](auto t) {
         with_type(grad_type, [&](auto o) {
-            with_bool(da.threshold != 0, [&](auto drop) {
-                using T = decltype(t);
-                using G = decltype(o);
-                hipLaunchKernelGGL((k_grad<T, G, decltype(drop)::value>), dim3((unsigned)blocks), dim3(kGradBlock), 0,
-                                   stream, static_cast<const T*>(dy), key, pos, g, c0, da, static_cast<G*>(grad), part);
+            with_bool(accumulate != 0, [&](auto acc) {
+                with_bool(da.threshold != 0, [&](auto drop) {
+                    using T = decltype(t);
+                    using G = decltype(o);
+                    hipLaunchKernelGGL((k_grad<T, G, decltype(acc)::value, decltype(drop)::value>),
+                                       dim3((unsigned)sum_blocks), dim3(kGradBlock), 0, stream,
+                                       static_cast<const T*>(dy), key, pos, g, c0, da, static_cast<G*>(grad), part);
+                });
             });
         });
     });
     if ((rc = launched(who))) return rc;
-    if (g.chunks < 2) return GSZ_OK;
-    int64_t step = 1;
-    for (; g.chunks > 2 * kFold * step; step *= kFold) {
-        const int64_t groups = (g.chunks + kFold * step - 1) / (kFold * step);
-        hipLaunchKernelGGL(k_fold, dim3((unsigned)(groups * j.col_blocks)), dim3(kGradBlock), 0, stream, key, j, step, part);
-        if ((rc = launched(who))) return rc;
-    }
     with_type(grad_type, [&](auto o) {
-        using G = decltype(o);
-        hipLaunchKernelGGL((k_join<G>), dim3((unsigned)(g.chunks * j.col_blocks)), dim3(kGradBlock), 0, stream, key, j,
-                           step, c0, static_cast<G*>(grad), static_cast<const float*>(part));
+        with_bool(accumulate != 0, [&](auto acc) {
+            using G = decltype(o);
+            hipLaunchKernelGGL((k_join<G, decltype(acc)::value>), dim3((unsigned)join_blocks), dim3(kJoinBlock), 0,
+                               stream, key, g, join_tiles, c0, static_cast<G*>(grad), static_cast<const float*>(part));
+        });
     });
     return launched(who);
 }

@@ -427,9 +427,9 @@ int gsz_embedding_lookup(const void* table, int32_t table_type, int64_t rows, in
                          hipStream_t stream);
 
 /* *out = bytes of device scratch gsz_embedding_grad needs for these sizes, per call
- * in flight (two captured graphs that may run at once need one each): the sorted
- * tokens and fp32 partial sums of rows with many tokens, at most about one fp32 per
- * gradient value for small n and an eighth of that for large n.  Needs no
+ * in flight (two captured graphs that may run at once need one each): none for n <= 128,
+ * else the sorted tokens, fp32 partial sums of rows with many tokens (n * dim bytes for
+ * small n, a quarter of that for large n) and, for n > 8192, 4 bytes a row.  Needs no
  * initialisation.  Errors as gsz_embedding_lookup's sizes. */
 int gsz_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim, size_t* out);
 
@@ -445,8 +445,8 @@ int gsz_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim, size_t* 
  *   dy (device, n * dim of dy_type); grad (device, rows * dim of grad_type): both any
  *     multiple of the value's size, so grad may be a tensor's place in a bf16 or fp32
  *     bucket-flat buffer.  It must not overlap dy or ids.
- *   ws (device, 16-byte aligned, >= gsz_embedding_workspace_bytes): scratch, required
- *     unless n or dim is 0 (GSZ_ERR_SIZE if too small).
+ *   ws (device, 16-byte aligned, >= gsz_embedding_workspace_bytes): scratch (GSZ_ERR_SIZE
+ *     if too small); may be NULL where none is needed.
  * Errors as gsz_embedding_lookup; GSZ_ERR_SIZE too if a launch would need more than
  * 2^31 work-items (n * dim over about 2^39, or n over 2^29). */
 int gsz_embedding_grad(const void* ids, int32_t id_type, int64_t n, const void* dy, int32_t dy_type,

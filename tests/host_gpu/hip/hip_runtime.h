@@ -104,7 +104,7 @@ template <class F> void launch(unsigned grid, unsigned block, F body) {
         }
     }
 }
-struct Idx { int which; operator unsigned() const { return which == 0 ? (unsigned)S.cur : which == 1 ? S.bx : S.gx; } };
+struct Idx { int which; operator unsigned() const { return which == 0 ? (unsigned)S.cur : which == 1 ? S.bx : which == 2 ? S.gx : S.dimx; } };
 struct Dim { Idx x; };
 inline uint64_t exchange(uint64_t v, std::function<uint64_t()> read) {
     S.slot[S.cur] = v;
@@ -119,7 +119,7 @@ inline uint32_t read_lane(uint32_t v, int lane) {
 }
 }  // namespace emu
 
-static const emu::Dim threadIdx{{0}}, blockIdx{{1}}, gridDim{{2}};
+static const emu::Dim threadIdx{{0}}, blockIdx{{1}}, gridDim{{2}}, blockDim{{3}};
 inline void __syncthreads() { emu::sync(emu::S.block); }
 inline uint64_t __ballot(bool b) {
     return emu::exchange(b, [] {
@@ -136,6 +136,10 @@ inline float __uint_as_float(uint32_t u) { float f; std::memcpy(&f, &u, 4); retu
 inline uint32_t __float_as_uint(float f) { uint32_t u; std::memcpy(&u, &f, 4); return u; }
 inline uint32_t __umulhi(uint32_t a, uint32_t b) { return (uint32_t)((uint64_t)a * b >> 32); }
 inline uint32_t __shfl(uint32_t v, int lane) { return emu::read_lane(v, lane); }
+inline uint32_t __shfl_up(uint32_t v, int delta) {
+    const int lane = emu::S.cur & 63;
+    return emu::read_lane(v, lane >= delta ? lane - delta : lane);
+}
 #define __builtin_amdgcn_fence(...) ((void)0)
 #define __builtin_amdgcn_wave_barrier() emu::sync(emu::wave())
 #define __builtin_amdgcn_readlane(v, lane) emu::read_lane((v), (lane))

@@ -244,7 +244,7 @@ def check_grad(n, rows, dim, kind="any", dt=BF, gt=BF, it=torch.int64, acc=False
     assert torch.equal(again.t, g.t)
 
 
-@pytest.mark.parametrize("n", [0, 1, 2, 5, 63, 64, 65, 200, 511])
+@pytest.mark.parametrize("n", [0, 1, 2, 5, 63, 64, 65, 127, 128, 129, 200, 511])
 @pytest.mark.parametrize("kind", ["any", "one", "none", "distinct"])
 @pytest.mark.parametrize("acc", [False, True])
 def test_grad_small(n, kind, acc):
@@ -433,7 +433,7 @@ def test_offsets_past_32_bits():
 
 
 def test_refuses_tensors_of_host_and_bad_workspace():
-    ids, dy = torch.zeros(4, dtype=torch.int64, device="cuda"), torch.zeros(4, 8, dtype=BF, device="cuda")
+    ids, dy = torch.zeros(200, dtype=torch.int64, device="cuda"), torch.zeros(200, 8, dtype=BF, device="cuda")
     grad = torch.zeros(3, 8, dtype=BF, device="cuda")
     with pytest.raises(ValueError, match="device tensor"):
         G.embedding_lookup(ids.cpu(), grad, dy)

@@ -49,8 +49,8 @@ NAN, INF = float("nan"), float("inf")
     (grad, dict(rows=1 << 31), SIZE), (grad, dict(n=1 << 31), SIZE), (grad, dict(dim=1 << 30), SIZE),
     (grad, dict(acc=2), INVALID), (grad, dict(p=1.5), INVALID), (grad, dict(p=0.1), INVALID),
     (grad, dict(scale=-INF), INVALID), (grad, dict(dy=None), INVALID), (grad, dict(ids=None), INVALID),
-    (grad, dict(g=None), INVALID), (grad, dict(ws=None), SIZE), (grad, dict(ws_bytes=16), SIZE),
-    (grad, dict(ws=BUF + 8), MISALIGNED), (grad, dict(dy=BUF + 1), MISALIGNED),
+    (grad, dict(g=None), INVALID), (grad, dict(n=129, ws=None), SIZE), (grad, dict(n=129, ws_bytes=16), SIZE),
+    (grad, dict(n=129, ws=BUF + 8), MISALIGNED), (grad, dict(dy=BUF + 1), MISALIGNED),
     (grad, dict(gt=F32, g=BUF + 2), MISALIGNED), (grad, dict(ids=BUF + 4), MISALIGNED),
     # more work-items than one launch holds: refused before the sort is enqueued
     (grad, dict(n=(1 << 31) - 1, ws_bytes=1 << 62), SIZE),
@@ -71,9 +71,10 @@ def test_workspace_bytes():
     for n, rows, dim in ((1, 1, 1), (8192, 50257, 768), (8193, 50257, 768), (65536, 32000, 8192),
                          (300_000, 5, 4), (1 << 22, 1 << 30, 1)):
         b = G.embedding_workspace_bytes(n, rows, dim)
-        assert b % 256 == 0 and b >= 8 * n
-        # sorted pairs twice, three digit tables, two fp32 partial rows per chunk of at least 8 tokens
-        assert b <= 16 * n + 3 * 4 * 256 * 1024 + 8 * (-(-n // 8)) * (dim + 7) + 4096
+        # none for up to 128 tokens; else sorted pairs twice, a digit table, a token of
+        # each row, two fp32 partial rows per chunk of at least 8 tokens
+        assert b % 256 == 0 and (b >= 8 * n if n > 128 else b == 0)
+        assert b <= 16 * n + 4 * 256 * 1024 + 4 * rows + 8 * (-(-n // 8)) * (dim + 7) + 4096
     for bad in ((-1, 1, 1), (1, -1, 1), (1, 1, -1), (1 << 31, 1, 1), (1, 1 << 31, 1), (1, 1, 1 << 30)):
         with pytest.raises(G.GszError):
             G.embedding_workspace_bytes(*bad)
