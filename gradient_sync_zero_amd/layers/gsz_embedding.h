@@ -21,81 +21,81 @@ __device__ __forceinline__ uint32_t row_of(const Ids& ids, int64_t i) {
 // ---------------------------------------------------------------- lookup --
 
 // out[i, c] = id_i is a row and not dropped(i * dim + c) ? table[id_i, c] * c0 : 0.
-// A row is vpr = ceil(dim / 8) vectors, cut into `slices` column slices of at most sv
-// vectors; a block takes tile_rows rows of one slice, up to kLookVecs vectors, with
-// kLookUnroll loads of the table in flight per lane and then the stores.  Block b has
-// slice b mod slices: blocks go to the eight XCDs in turn, so with eight slices each
-// XCD's L2 holds its own columns of the rows that come often, eight times as many
-// rows as if every XCD read whole ones.
-// magic = floor(2^32 / sv) + 1: (q * magic) >> 32 == q / sv for q, sv <= kLookVecs;
-// wider slices come one row to a block.
-constexpr int kLookBlock = 256, kLookUnroll = 4, kLookVecs = kLookBlock * kLookUnroll;
-struct LookShape { int64_t n, dim, vpr, sv, tiles; uint64_t magic; int slices, tile_rows; };
+//
+// A row is vpr = ceil(dim / 8) vectors.  A lane keeps its column and takes up to
+// kLookUnroll rows, whose loads are in flight together before the first store; the
+// work per vector has to stay near the 20 instructions of widening, scaling and
+// rounding, or the VALU and not the memory sets the pace (with each lane finding row
+// and column of every vector anew, 64 Ki tokens of 8192 columns took 368 us, and
+// the same reads without the stores already 211).
+// WIDE (vpr > kLookBlock / 2): a block takes one of `cols` column blocks of `width`
+// vectors, and its rows are the same for all lanes.  Else a block holds `side` rows
+// side by side, lane t being vector t mod vpr of row t / vpr; magic =
+// floor(2^32 / vpr) + 1, so (t * magic) >> 32 == t / vpr.
+constexpr int kLookBlock = 256, kLookUnroll = 4;
+struct LookShape { int64_t n, dim, tiles; uint64_t magic; int vpr, cols, width, side, per; };
 
-template <typename T, typename O, bool DROP>
+template <typename T, typename O, bool DROP, bool WIDE>
 __global__ __launch_bounds__(kLookBlock) void k_lookup(const T* __restrict__ table, Ids ids, LookShape s,
                                                        float c0, DropArgs da, O* __restrict__ out) {
     DropKey d{};
     if (DROP) d = drop_key(da);
-    const int64_t blocks = s.tiles * s.slices;
+    const int tid = threadIdx.x;
+    const int64_t blocks = s.tiles * s.cols;
     for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
-        const int64_t tile = s.slices == 1 ? b : b / s.slices, v0 = s.slices == 1 ? 0 : (b % s.slices) * s.sv;
-        const int64_t width = s.vpr - v0 < s.sv ? s.vpr - v0 : s.sv;      // vectors of this slice
-        const int64_t row0 = tile * s.tile_rows;
-        const int64_t nrows = s.n - row0 < s.tile_rows ? s.n - row0 : s.tile_rows;
-        const int64_t vecs = nrows * s.sv;
-        for (int64_t q0 = threadIdx.x; q0 < vecs; q0 += kLookVecs) {
-            Raw8<T> r[kLookUnroll];
-            int64_t row[kLookUnroll], col[kLookUnroll];
-            bool is_row[kLookUnroll];
+        int64_t tile = b;
+        int v = tid, lr = 0;
+        if (WIDE) {
+            tile = s.cols == 1 ? b : b / s.cols;
+            const int v0 = (int)(b - tile * s.cols) * s.width;
+            v += v0;
+            if (tid >= s.width || v >= s.vpr) continue;
+        } else {
+            lr = (int)(((uint64_t)tid * s.magic) >> 32);
+            v -= lr * s.vpr;
+            if (lr >= s.side) continue;
+        }
+        const int64_t col = 8 * (int64_t)v, row0 = tile * (s.side * s.per) + lr;
+        const bool whole = s.dim - col >= 8;
+        const int left = whole ? 8 : (int)(s.dim - col);
+        Raw8<T> r[kLookUnroll];
+        bool in[kLookUnroll], is_row[kLookUnroll];
 #pragma unroll
-            for (int u = 0; u < kLookUnroll; ++u) {
-                const int64_t q = q0 + u * kLookBlock;
-                is_row[u] = false;
-                row[u] = -1;
-                col[u] = 0;
-                if (q < vecs) {
-                    const int64_t lr = s.tile_rows == 1 ? 0 : (int64_t)(((uint64_t)q * s.magic) >> 32);
-                    const int64_t v = q - lr * s.sv;
-                    if (v < width) {
-                        row[u] = row0 + lr;
-                        col[u] = 8 * (v0 + v);
-                        const uint32_t id = row_of(ids, row[u]);
-                        is_row[u] = id != ids.rows;
-                        if (is_row[u]) {
-                            const T* p = table + (int64_t)id * s.dim + col[u];
-                            const int64_t left = s.dim - col[u];
-                            r[u] = left >= 8 ? load8<false>(p) : load8_part(p, (int)left);
-                        }
-                    }
-                }
-            }
-            // The masks need no data: they are drawn while the loads are on their way, in
-            // a loop of its own that holds the generator's code once.
-            uint32_t gone = 0;
-            if (DROP) {
-#pragma unroll 1
-                for (int u = 0; u < kLookUnroll && q0 + u * kLookBlock < vecs; ++u) {
-                    const int64_t q = q0 + u * kLookBlock;
-                    const int64_t lr = s.tile_rows == 1 ? 0 : (int64_t)(((uint64_t)q * s.magic) >> 32);
-                    gone |= dropped8(d, (uint64_t)((row0 + lr) * s.dim + 8 * (v0 + q - lr * s.sv))) << 8 * u;
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kLookUnroll; ++u) {
-                if (row[u] < 0) continue;
-                float a[8] = {};
+        for (int u = 0; u < kLookUnroll; ++u) {
+            const int64_t row = row0 + u * s.side;
+            in[u] = u < s.per && row < s.n;
+            is_row[u] = false;
+            if (in[u]) {
+                uint32_t id = row_of(ids, row);
+                if (WIDE) id = __builtin_amdgcn_readfirstlane(id);
+                is_row[u] = id != ids.rows;
                 if (is_row[u]) {
-                    widen(r[u], a);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) a[j] = a[j] * c0;
-                    if (DROP) drop8(gone >> 8 * u, a);
+                    const T* p = table + (int64_t)id * s.dim + col;
+                    r[u] = whole ? load8<false>(p) : load8_part(p, left);
                 }
-                O* p = out + row[u] * s.dim + col[u];
-                const int64_t left = s.dim - col[u];
-                if (left >= 8) store8<true>(p, a);
-                else store8_part(p, a, (int)left);
             }
+        }
+        // The masks need no data: they are drawn while the loads are on their way, in
+        // a loop of their own that holds the generator's code once.
+        uint32_t gone = 0;
+        if (DROP) {
+#pragma unroll 1
+            for (int u = 0; u < s.per; ++u)
+                gone |= dropped8(d, (uint64_t)((row0 + u * s.side) * s.dim + col)) << 8 * u;
+        }
+#pragma unroll
+        for (int u = 0; u < kLookUnroll; ++u) {
+            if (!in[u]) continue;
+            float a[8] = {};
+            if (is_row[u]) {
+                widen(r[u], a);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) a[j] = a[j] * c0;
+                if (DROP) drop8(gone >> 8 * u, a);
+            }
+            O* p = out + (row0 + u * s.side) * s.dim + col;
+            if (whole) store8<true>(p, a);
+            else store8_part(p, a, left);
         }
     }
 }

@@ -194,24 +194,29 @@ extern "C" int gsz_embedding_lookup(const void* table, int32_t table_type, int64
     LookShape l{};
     l.n = n;
     l.dim = dim;
-    l.vpr = (dim + 7) / 8;
-    l.slices = 8;
-    while (l.slices > 1 && l.vpr / l.slices < 64) l.slices /= 2;      // a wave's load stays in one row
-    l.sv = (l.vpr + l.slices - 1) / l.slices;
-    int64_t vecs = kLookVecs;                                         // per block
-    while (vecs > kLookBlock && n * l.vpr / vecs < 2048) vecs /= 2;
-    l.tile_rows = l.sv >= vecs ? 1 : (int)(vecs / l.sv);
-    l.magic = ((uint64_t)1 << 32) / (uint64_t)l.sv + 1;
-    l.tiles = (n + l.tile_rows - 1) / l.tile_rows;
-    const int grid = grid_for(l.tiles * l.slices, kLookBlock);
+    l.vpr = (int)((dim + 7) / 8);
+    const bool wide = l.vpr > kLookBlock / 2;
+    l.cols = wide ? (l.vpr + kLookBlock - 1) / kLookBlock : 1;
+    l.width = (l.vpr + l.cols - 1) / l.cols;
+    l.side = wide ? 1 : kLookBlock / l.vpr;
+    l.magic = ((uint64_t)1 << 32) / (uint64_t)l.vpr + 1;
+    // Rows per lane: one where a few thousand blocks are all there is.
+    l.per = kLookUnroll;
+    while (l.per > 1 && (n + (int64_t)l.side * l.per - 1) / ((int64_t)l.side * l.per) * l.cols < 4096) l.per /= 2;
+    l.tiles = (n + (int64_t)l.side * l.per - 1) / ((int64_t)l.side * l.per);
+    const int block = ((wide ? l.width : l.side * l.vpr) + 63) / 64 * 64;
+    const int grid = grid_for(l.tiles * l.cols, kLookBlock);
     const Ids id{ids, id_type == GSZ_TYPE_I64, (uint32_t)rows};
     with_type(table_type, [&](auto t) {
         with_type(out_type, [&](auto o) {
             with_bool(da.threshold != 0, [&](auto drop) {
-                using T = decltype(t);
-                using O = decltype(o);
-                hipLaunchKernelGGL((k_lookup<T, O, decltype(drop)::value>), dim3(grid), dim3(kLookBlock), 0,
-                                   stream, static_cast<const T*>(table), id, l, c0, da, static_cast<O*>(out));
+                with_bool(wide, [&](auto w) {
+                    using T = decltype(t);
+                    using O = decltype(o);
+                    hipLaunchKernelGGL((k_lookup<T, O, decltype(drop)::value, decltype(w)::value>), dim3(grid),
+                                       dim3(block), 0, stream, static_cast<const T*>(table), id, l, c0, da,
+                                       static_cast<O*>(out));
+                });
             });
         });
     });
