@@ -22,18 +22,20 @@ __device__ __forceinline__ uint32_t row_of(const Ids& ids, int64_t i) {
 
 // out[i, c] = id_i is a row and not dropped(i * dim + c) ? table[id_i, c] * c0 : 0.
 //
-// A row is vpr = ceil(dim / 8) vectors.  A lane keeps its column and takes up to
-// kLookUnroll rows, whose loads are in flight together before the first store; the
-// work per vector has to stay near the 20 instructions of widening, scaling and
-// rounding, or the VALU and not the memory sets the pace (with each lane finding row
-// and column of every vector anew, 64 Ki tokens of 8192 columns took 368 us, and
-// the same reads without the stores already 211).
-// WIDE (vpr > kLookBlock / 2): a block takes one of `cols` column blocks of `width`
-// vectors, and its rows are the same for all lanes.  Else a block holds `side` rows
-// side by side, lane t being vector t mod vpr of row t / vpr; magic =
-// floor(2^32 / vpr) + 1, so (t * magic) >> 32 == t / vpr.
+// A row is vpr = ceil(dim / 8) vectors.  A lane takes up to kLookUnroll vectors at fixed
+// distances, whose loads are in flight together before the first store; the work per
+// vector has to stay near the 20 instructions of widening, scaling and rounding, or the
+// VALU and not the memory sets the pace (with each lane finding row and column of
+// every vector anew, 64 Ki tokens of 8192 columns took 368 us, and the same reads
+// without the stores already 211).
+// WIDE (vpr > kLookBlock / 2): the rows of a block are the same for all its lanes; a
+// row is cut into column blocks of `width` <= kLookBlock vectors, and a block takes
+// 2^wide_log2 of them in each of `per` rows: as much of a row as it can, so that
+// blocks in order write memory in order.
+// Else a block holds `side` rows side by side, lane t being vector t mod vpr of row
+// t / vpr, `per` times; magic = floor(2^32 / vpr) + 1, so (t * magic) >> 32 == t / vpr.
 constexpr int kLookBlock = 256, kLookUnroll = 4;
-struct LookShape { int64_t n, dim, tiles; uint64_t magic; int vpr, cols, width, side, per; };
+struct LookShape { int64_t n, dim, tiles; uint64_t magic; int vpr, cols, width, wide_log2, side, per; };
 
 template <typename T, typename O, bool DROP, bool WIDE>
 __global__ __launch_bounds__(kLookBlock) void k_lookup(const T* __restrict__ table, Ids ids, LookShape s,
@@ -46,33 +48,35 @@ __global__ __launch_bounds__(kLookBlock) void k_lookup(const T* __restrict__ tab
         int64_t tile = b;
         int v = tid, lr = 0;
         if (WIDE) {
+            if (tid >= s.width) return;
             tile = s.cols == 1 ? b : b / s.cols;
-            const int v0 = (int)(b - tile * s.cols) * s.width;
-            v += v0;
-            if (tid >= s.width || v >= s.vpr) continue;
+            v += ((int)(b - tile * s.cols) << s.wide_log2) * s.width;
         } else {
             lr = (int)(((uint64_t)tid * s.magic) >> 32);
             v -= lr * s.vpr;
-            if (lr >= s.side) continue;
+            if (lr >= s.side) return;
         }
-        const int64_t col = 8 * (int64_t)v, row0 = tile * (s.side * s.per) + lr;
-        const bool whole = s.dim - col >= 8;
-        const int left = whole ? 8 : (int)(s.dim - col);
+        const int64_t row0 = tile * (s.side * s.per) + lr;
+        // The u-th vector's row and first column.
+        auto row_at = [&](int u) -> int64_t { return row0 + (WIDE ? u >> s.wide_log2 : u) * s.side; };
+        auto col_at = [&](int u) -> int64_t {
+            return 8 * (int64_t)(WIDE ? v + (u & ((1 << s.wide_log2) - 1)) * s.width : v);
+        };
+        const int vectors = WIDE ? s.per << s.wide_log2 : s.per;
         Raw8<T> r[kLookUnroll];
         bool in[kLookUnroll], is_row[kLookUnroll];
 #pragma unroll
         for (int u = 0; u < kLookUnroll; ++u) {
-            const int64_t row = row0 + u * s.side;
-            in[u] = u < s.per && row < s.n;
-            is_row[u] = false;
-            if (in[u]) {
-                uint32_t id = row_of(ids, row);
-                if (WIDE) id = __builtin_amdgcn_readfirstlane(id);
-                is_row[u] = id != ids.rows;
-                if (is_row[u]) {
-                    const T* p = table + (int64_t)id * s.dim + col;
-                    r[u] = whole ? load8<false>(p) : load8_part(p, left);
-                }
+            const int64_t row = row_at(u), col = col_at(u), left = s.dim - col;
+            in[u] = is_row[u] = false;
+            if (u >= vectors || row >= s.n) continue;
+            uint32_t id = row_of(ids, row);
+            if (WIDE) id = __builtin_amdgcn_readfirstlane(id);
+            in[u] = left > 0;
+            is_row[u] = in[u] && id != ids.rows;
+            if (is_row[u]) {
+                const T* p = table + (int64_t)id * s.dim + col;
+                r[u] = left >= 8 ? load8<false>(p) : load8_part(p, (int)left);
             }
         }
         // The masks need no data: they are drawn while the loads are on their way, in
@@ -80,8 +84,8 @@ __global__ __launch_bounds__(kLookBlock) void k_lookup(const T* __restrict__ tab
         uint32_t gone = 0;
         if (DROP) {
 #pragma unroll 1
-            for (int u = 0; u < s.per; ++u)
-                gone |= dropped8(d, (uint64_t)((row0 + u * s.side) * s.dim + col)) << 8 * u;
+            for (int u = 0; u < vectors; ++u)
+                gone |= dropped8(d, (uint64_t)(row_at(u) * s.dim + col_at(u))) << 8 * u;
         }
 #pragma unroll
         for (int u = 0; u < kLookUnroll; ++u) {
@@ -93,9 +97,10 @@ __global__ __launch_bounds__(kLookBlock) void k_lookup(const T* __restrict__ tab
                 for (int j = 0; j < 8; ++j) a[j] = a[j] * c0;
                 if (DROP) drop8(gone >> 8 * u, a);
             }
-            O* p = out + (row0 + u * s.side) * s.dim + col;
-            if (whole) store8<true>(p, a);
-            else store8_part(p, a, left);
+            const int64_t col = col_at(u), left = s.dim - col;
+            O* p = out + row_at(u) * s.dim + col;
+            if (left >= 8) store8<true>(p, a);
+            else store8_part(p, a, (int)left);
         }
     }
 }

@@ -196,13 +196,19 @@ extern "C" int gsz_embedding_lookup(const void* table, int32_t table_type, int64
     l.dim = dim;
     l.vpr = (int)((dim + 7) / 8);
     const bool wide = l.vpr > kLookBlock / 2;
-    l.cols = wide ? (l.vpr + kLookBlock - 1) / kLookBlock : 1;
-    l.width = (l.vpr + l.cols - 1) / l.cols;
+    // Vectors per lane: fewer where a few thousand blocks are all there is.
+    int vectors = kLookUnroll;
+    while (vectors > 1 && n * l.vpr / (kLookBlock * vectors) < 4096) vectors /= 2;
     l.side = wide ? 1 : kLookBlock / l.vpr;
+    l.per = vectors;
+    l.cols = 1;
+    if (wide) {
+        const int pieces = (l.vpr + kLookBlock - 1) / kLookBlock;     // of at most kLookBlock vectors
+        while (l.per > 1 && 2 << l.wide_log2 <= pieces) { ++l.wide_log2; l.per /= 2; }
+        l.width = (l.vpr + pieces - 1) / pieces;
+        l.cols = (pieces + (1 << l.wide_log2) - 1) >> l.wide_log2;
+    }
     l.magic = ((uint64_t)1 << 32) / (uint64_t)l.vpr + 1;
-    // Rows per lane: one where a few thousand blocks are all there is.
-    l.per = kLookUnroll;
-    while (l.per > 1 && (n + (int64_t)l.side * l.per - 1) / ((int64_t)l.side * l.per) * l.cols < 4096) l.per /= 2;
     l.tiles = (n + (int64_t)l.side * l.per - 1) / ((int64_t)l.side * l.per);
     const int block = ((wide ? l.width : l.side * l.vpr) + 63) / 64 * 64;
     const int grid = grid_for(l.tiles * l.cols, kLookBlock);
