@@ -111,16 +111,27 @@ __global__ __launch_bounds__(kLookBlock) void k_lookup(const T* __restrict__ tab
 // that: the blocks that clear ride along with the sort, whose few blocks leave
 // the memory idle.
 
-// Clears the rows r0 + i, i a set bit of `missing`, with the whole block.
+// Clears the rows r0 + i, i a set bit of `missing`, with the whole block: neighbours
+// as one stretch of memory in whole 16-byte vectors, whatever the rows' alignment (row by
+// row at the rows' own places, 31,000 rows of 4097 fp32 took 210 us, 2.5 TB/s).
 template <typename G>
 __device__ __forceinline__ void clear_rows(G* __restrict__ grad, int64_t dim, int64_t r0, uint64_t missing) {
-    const float zero[8] = {};
-    for (uint64_t m = missing; m; m &= m - 1) {
-        G* p = grad + (r0 + __builtin_ctzll(m)) * dim;
-        for (int64_t c = 8 * (int64_t)threadIdx.x; c < dim; c += 8 * (int64_t)blockDim.x) {
-            if (dim - c >= 8) store8<true>(p + c, zero);
-            else store8_part(p + c, zero, (int)(dim - c));
-        }
+    while (missing) {
+        const int first = __builtin_ctzll(missing);
+        const uint64_t rest = ~(missing >> first);
+        const int count = rest ? __builtin_ctzll(rest) : 64;
+        missing = first + count >= 64 ? 0 : missing >> (first + count) << (first + count);
+        G* p = grad + (r0 + first) * dim;
+        const int64_t n = count * dim;
+        int64_t head = (16 - (reinterpret_cast<uintptr_t>(p) & 15)) % 16 / sizeof(G);
+        if (head > n) head = n;
+        const int64_t vecs = (n - head) * (int64_t)sizeof(G) / 16;
+        u32x4* q = reinterpret_cast<u32x4*>(p + head);
+        for (int64_t i = threadIdx.x; i < vecs; i += blockDim.x)
+            __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, q + i);
+        const int64_t tail = head + vecs * (16 / (int64_t)sizeof(G));
+        if ((int64_t)threadIdx.x < head) p[threadIdx.x] = 0;
+        if ((int64_t)threadIdx.x < n - tail) p[tail + threadIdx.x] = 0;
     }
 }
 
@@ -168,13 +179,18 @@ __global__ __launch_bounds__(kRankBlock) void k_rank(Ids ids, int n, uint32_t* _
     __shared__ uint32_t seen[64][2];
     const int tid = threadIdx.x;
     const int quads = (n + 4 * kRankSlices - 1) / (4 * kRankSlices) * kRankSlices;
-    for (int j = tid; j < 4 * quads; j += kRankBlock) {
-        uint32_t k = 0xFFFFFFFFu;
-        if (j < n) {
-            k = row_of(ids, j);
-            if (PACKED) k = k << kRankBits | (uint32_t)j;
+    {
+        uint32_t k[kRankMax / kRankBlock];            // the loads in flight together
+#pragma unroll
+        for (int u = 0; u < kRankMax / kRankBlock; ++u) {
+            const int j = tid + u * kRankBlock;
+            k[u] = j < n ? row_of(ids, j) : 0;
         }
-        all[j] = k;
+#pragma unroll
+        for (int u = 0; u < kRankMax / kRankBlock; ++u) {
+            const int j = tid + u * kRankBlock;
+            if (j < 4 * quads) all[j] = j >= n ? 0xFFFFFFFFu : PACKED ? k[u] << kRankBits | (uint32_t)j : k[u];
+        }
     }
     if (tid < 128) seen[tid >> 1][tid & 1] = 0;
     __syncthreads();
