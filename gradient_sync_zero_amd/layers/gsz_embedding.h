@@ -426,15 +426,19 @@ __device__ __forceinline__ f32x4 load4_nt(const float* p) {
 __device__ __forceinline__ f32x4 load4_part(const float* p, int64_t m) {
     return f32x4{m > 0 ? p[0] : 0.0f, m > 1 ? p[1] : 0.0f, m > 2 ? p[2] : 0.0f, m > 3 ? p[3] : 0.0f};
 }
-// row: the row's values at the tile's first column; left: columns from there on.
+// row: the row's values at the tile's first column; left: columns from there on, and
+// FULL where the tile has them all (most do, and the code for the others, eight times
+// unrolled, would not fit the instruction cache beside it).
+template <bool FULL>
 __device__ __forceinline__ RowPiece<uint16_t> load_row(const uint16_t* row, int64_t left) {
     const int64_t c = piece_col<uint16_t>(0), m = left - c;
-    return {m >= 8 ? load8<true>(row + c) : load8_part(row + c, (int)(m > 0 ? m : 0))};
+    return {FULL || m >= 8 ? load8<true>(row + c) : load8_part(row + c, (int)(m > 0 ? m : 0))};
 }
+template <bool FULL>
 __device__ __forceinline__ RowPiece<float> load_row(const float* row, int64_t left) {
     const int64_t c = piece_col<float>(0), d = piece_col<float>(1);
-    return {left - c >= 4 ? load4_nt(row + c) : load4_part(row + c, left - c),
-            left - d >= 4 ? load4_nt(row + d) : load4_part(row + d, left - d)};
+    return {FULL || left - c >= 4 ? load4_nt(row + c) : load4_part(row + c, left - c),
+            FULL || left - d >= 4 ? load4_nt(row + d) : load4_part(row + d, left - d)};
 }
 __device__ __forceinline__ void widen_row(const RowPiece<uint16_t>& r, float a[8]) { widen(r.r, a); }
 __device__ __forceinline__ void widen_row(const RowPiece<float>& r, float a[8]) {
@@ -468,31 +472,31 @@ __device__ __forceinline__ void store4(uint16_t* p, const float a[4]) {
     *reinterpret_cast<u32x2_at2*>(p) = u32x2{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
 }
 // The lane's old values of a row of grad.
-template <typename T, typename G>
+template <typename T, bool FULL, typename G>
 __device__ __forceinline__ void load_old(const G* row, int64_t left, float a[8]) {
-    if (Cols<T>::kPieces == 1 && left - piece_col<T>(0) >= 8) {
+    if (Cols<T>::kPieces == 1 && (FULL || left - piece_col<T>(0) >= 8)) {
         widen(load8<false>(row + piece_col<T>(0)), a);
         return;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int64_t c = Cols<T>::kPieces == 1 ? piece_col<T>(0) + 4 * h : piece_col<T>(h), m = left - c;
-        if (m >= 4) load4(row + c, a + 4 * h);
+        if (FULL || m >= 4) load4(row + c, a + 4 * h);
         else
 #pragma unroll
             for (int j = 0; j < 4; ++j) a[4 * h + j] = j < m ? load1(row + c + j) : 0.0f;
     }
 }
-template <typename T, typename G>
+template <typename T, bool FULL, typename G>
 __device__ __forceinline__ void store_row(G* row, int64_t left, const float a[8]) {
-    if (Cols<T>::kPieces == 1 && left - piece_col<T>(0) >= 8) {
+    if (Cols<T>::kPieces == 1 && (FULL || left - piece_col<T>(0) >= 8)) {
         store8<false>(row + piece_col<T>(0), a);
         return;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int64_t c = Cols<T>::kPieces == 1 ? piece_col<T>(0) + 4 * h : piece_col<T>(h), m = left - c;
-        if (m >= 4) store4(row + c, a + 4 * h);
+        if (FULL || m >= 4) store4(row + c, a + 4 * h);
         else
 #pragma unroll
             for (int j = 0; j < 4; ++j) if (j < m) store1(row + c + j, a[4 * h + j]);
@@ -506,88 +510,98 @@ struct GradShape {
     int K, tiles;                        // tiles of columns
 };
 
-template <typename T, typename G, bool ACC, bool DROP>
-__global__ __launch_bounds__(kGradBlock) void k_grad(const T* __restrict__ dy, const uint32_t* __restrict__ key,
-                                                     const uint32_t* __restrict__ pos, GradShape s,
-                                                     float c0, DropArgs da, G* __restrict__ grad,
-                                                     float* __restrict__ part) {
-    const int lane = threadIdx.x & 63;
-    const int64_t w = (int64_t)blockIdx.x * kGradWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t chunk = w / s.tiles;
-    if (chunk >= s.chunks) return;
-    const int64_t c = (w - chunk * s.tiles) * kGradCols, left = s.dim - c;
-    const int64_t s0 = chunk * s.K, s1 = s0 + s.K;
-    // Lane l holds the key and position of token s0 + l, l < 2 K.
-    uint32_t my_key = s.rows, my_pos = 0;
-    if (lane < 2 * s.K && s0 + lane < s.n) { my_key = key[s0 + lane]; my_pos = pos[s0 + lane]; }
-    const uint32_t none = 0xFFFFFFFFu;                               // no row's number
-    const uint32_t before = s0 > 0 ? key[s0 - 1] : none, long_before = s0 > s.K ? key[s0 - s.K - 1] : none;
-    const uint32_t after = s1 + s.K < s.n ? key[s1 + s.K] : none;
-    const uint32_t k_first = __builtin_amdgcn_readlane(my_key, 0), k_last = __builtin_amdgcn_readlane(my_key, s.K - 1);
-    const uint32_t k_next = __builtin_amdgcn_readlane(my_key, s.K), k_past = after;
-    int first = 0, last = __popcll(__ballot(lane < s.K && my_key != s.rows));
-    bool head_part = false, tail_part = false;
-    if (k_first == before) {                                         // a run goes on from the last chunk
-        if (long_before != k_first && k_next != k_first)             // that chunk finishes it
-            first = __popcll(__ballot(lane < s.K && my_key == k_first));
-        else head_part = true;
-    }
-    if (k_last == k_next && s.K == last) {                           // a run goes on into the next
-        if (k_last != before && k_past != k_last) last += __popcll(__ballot(lane >= s.K && my_key == k_last));
-        else tail_part = k_last != before;
-    }
-    if (first >= last) return;
-    DropKey d{};
-    if (DROP) d = drop_key(da);
+// The tokens [first, last) of a wave's chunk: lane l holds token l's key and position.
+struct GradWave { int64_t chunk, c, left; int first, last; bool head_part, tail_part; uint32_t key, pos; };
+
+template <typename T, typename G, bool ACC, bool DROP, bool FULL>
+__device__ __forceinline__ void grad_wave(const T* __restrict__ dy, const GradShape& s, GradWave w, float c0,
+                                          const DropKey& d, G* __restrict__ grad, float* __restrict__ part) {
     float sum[8] = {};
-    for (int t = first; t < last; t += kGradUnroll) {
+    for (int t = w.first; t < w.last; t += kGradUnroll) {
         RowPiece<T> r[kGradUnroll];
         float old[ACC ? kGradUnroll : 1][8];
-        uint32_t kk[kGradUnroll], pp[kGradUnroll];
+        uint32_t kk[kGradUnroll];
         bool ends[kGradUnroll];
 #pragma unroll
         for (int u = 0; u < kGradUnroll; ++u) {
-            const int at = t + u < last ? t + u : last - 1;
-            kk[u] = __builtin_amdgcn_readlane(my_key, at);
-            pp[u] = __builtin_amdgcn_readlane(my_pos, at);
-            ends[u] = at + 1 == last || (uint32_t)__builtin_amdgcn_readlane(my_key, at + 1) != kk[u];
-            if (t + u < last) r[u] = load_row(dy + (int64_t)pp[u] * s.dim + c, left);
-            if (ACC && t + u < last && ends[u]) load_old<T>(grad + (int64_t)kk[u] * s.dim + c, left, old[u]);
+            const int at = t + u < w.last ? t + u : w.last - 1;
+            kk[u] = __builtin_amdgcn_readlane(w.key, at);
+            const uint32_t p = __builtin_amdgcn_readlane(w.pos, at);
+            ends[u] = at + 1 == w.last || (uint32_t)__builtin_amdgcn_readlane(w.key, at + 1) != kk[u];
+            if (t + u < w.last) r[u] = load_row<FULL>(dy + (int64_t)p * s.dim + w.c, w.left);
+            if (ACC && t + u < w.last && ends[u])
+                load_old<T, FULL>(grad + (int64_t)kk[u] * s.dim + w.c, w.left, old[u]);
         }
         uint32_t gone[2] = {};                                       // 8 bits for each u
         if (DROP) {
 #pragma unroll 1
-            for (int u = 0; u < kGradUnroll && t + u < last; ++u) {
-                const uint32_t p = __builtin_amdgcn_readlane(my_pos, t + u);
-                const uint32_t m = dropped_row<T>(d, (uint64_t)p * (uint64_t)s.dim + (uint64_t)c) << 8 * (u & 3);
+            for (int u = 0; u < kGradUnroll && t + u < w.last; ++u) {
+                const uint32_t p = __builtin_amdgcn_readlane(w.pos, t + u);
+                const uint32_t m = dropped_row<T>(d, (uint64_t)p * (uint64_t)s.dim + (uint64_t)w.c) << 8 * (u & 3);
                 gone[0] |= u < 4 ? m : 0;
                 gone[1] |= u < 4 ? 0 : m;
             }
         }
 #pragma unroll
         for (int u = 0; u < kGradUnroll; ++u) {
-            if (t + u >= last) break;
+            if (t + u >= w.last) break;
             float a[8];
             widen_row(r[u], a);
             if (DROP) drop8(gone[u >> 2] >> 8 * (u & 3), a);
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum[j] = sum[j] + a[j];
             if (!ends[u]) continue;
-            if (head_part || (tail_part && t + u + 1 == last)) {
-                store_row<T>(part + (2 * chunk + (head_part ? 0 : 1)) * s.pitch + c, s.pitch - c, sum);
+            if (w.head_part || (w.tail_part && t + u + 1 == w.last)) {
+                store_row<T, FULL>(part + (2 * w.chunk + (w.head_part ? 0 : 1)) * s.pitch + w.c, s.pitch - w.c, sum);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     a[j] = sum[j] * c0;
                     if (ACC) a[j] = old[ACC ? u : 0][j] + a[j];
                 }
-                store_row<T>(grad + (int64_t)kk[u] * s.dim + c, left, a);
+                store_row<T, FULL>(grad + (int64_t)kk[u] * s.dim + w.c, w.left, a);
             }
-            head_part = false;
+            w.head_part = false;
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
         }
     }
+}
+
+template <typename T, typename G, bool ACC, bool DROP>
+__global__ __launch_bounds__(kGradBlock) void k_grad(const T* __restrict__ dy, const uint32_t* __restrict__ key,
+                                                     const uint32_t* __restrict__ pos, GradShape s,
+                                                     float c0, DropArgs da, G* __restrict__ grad,
+                                                     float* __restrict__ part) {
+    const int lane = threadIdx.x & 63;
+    const int64_t wave = (int64_t)blockIdx.x * kGradWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t chunk = wave / s.tiles;
+    if (chunk >= s.chunks) return;
+    const int64_t c = (wave - chunk * s.tiles) * kGradCols;
+    const int64_t s0 = chunk * s.K, s1 = s0 + s.K;
+    // Lane l holds the key and position of token s0 + l, l < 2 K.
+    uint32_t my_key = s.rows, my_pos = 0;
+    if (lane < 2 * s.K && s0 + lane < s.n) { my_key = key[s0 + lane]; my_pos = pos[s0 + lane]; }
+    const uint32_t none = 0xFFFFFFFFu;                               // no row's number
+    const uint32_t before = s0 > 0 ? key[s0 - 1] : none, long_before = s0 > s.K ? key[s0 - s.K - 1] : none;
+    const uint32_t past = s1 + s.K < s.n ? key[s1 + s.K] : none;
+    const uint32_t k_first = __builtin_amdgcn_readlane(my_key, 0), k_last = __builtin_amdgcn_readlane(my_key, s.K - 1);
+    const uint32_t k_next = __builtin_amdgcn_readlane(my_key, s.K);
+    GradWave w{chunk, c, s.dim - c, 0, (int)__popcll(__ballot(lane < s.K && my_key != s.rows)), false, false, my_key, my_pos};
+    if (k_first == before) {                                         // a run goes on from the last chunk
+        if (long_before != k_first && k_next != k_first)             // that chunk finishes it
+            w.first = __popcll(__ballot(lane < s.K && my_key == k_first));
+        else w.head_part = true;
+    }
+    if (k_last == k_next && s.K == w.last) {                         // a run goes on into the next
+        if (k_last != before && past != k_last) w.last += __popcll(__ballot(lane >= s.K && my_key == k_last));
+        else w.tail_part = k_last != before;
+    }
+    if (w.first >= w.last) return;
+    DropKey d{};
+    if (DROP) d = drop_key(da);
+    if (w.left >= kGradCols) grad_wave<T, G, ACC, DROP, true>(dy, s, w, c0, d, grad, part);
+    else grad_wave<T, G, ACC, DROP, false>(dy, s, w, c0, d, grad, part);
 }
 
 // Finishes the runs that k_grad left in parts.  A block looks at 64 chunks and takes
@@ -620,20 +634,25 @@ __global__ __launch_bounds__(kJoinBlock) void k_join(const uint32_t* __restrict_
     const int64_t c = c0l + 4 * lane, cp = c < s.pitch ? c : 0;        // lanes past the row read its start
     const int64_t mine = g * 64 + lane, e = (mine + 1) * s.K;        // this lane's chunk and its end
     uint32_t k = s.rows;
-    bool starts = false;
-    if (mine < s.chunks && e < s.n) {
+    bool starts = false, inside = false;                             // a run starts here, or comes from before;
+    if (mine < s.chunks && e < s.n) {                                // either way it goes on into the next chunk
         k = key[e - 1];
         const uint32_t next = key[e], before = mine > 0 ? key[e - s.K - 1] : 0xFFFFFFFFu;
         const uint32_t past = e + s.K < s.n ? key[e + s.K] : 0xFFFFFFFFu;
-        starts = k != s.rows && k == next && k != before && k == past;
+        const bool on = k != s.rows && k == next;
+        starts = on && k != before && k == past;
+        inside = on && k == before;
     }
+    const uint64_t through = __ballot(inside);
     int order = 0;
     for (uint64_t m = __ballot(starts); m; m &= m - 1, ++order) {
         const int l = __builtin_ctzll(m);
         const uint32_t row = __builtin_amdgcn_readlane(k, l);
         const int64_t chunk = g * 64 + l;
-        int64_t parts = 1;                                           // with the chunks that the run goes on into
-        for (;;) {
+        // The chunks of the run: this one, those that it passes through, its last.
+        const uint64_t ends = l < 63 ? ~through >> (l + 1) << (l + 1) : 0;
+        int64_t parts = (ends ? __builtin_ctzll(ends) : 64) - l + 1;
+        while (!ends) {                                              // on past the 64 chunks
             const int64_t j = chunk + parts + lane;
             const uint64_t on = __ballot(j < s.chunks && key[j < s.chunks ? j * s.K : 0] == row);
             const int more = ~on ? __builtin_ctzll(~on) : 64;
@@ -704,7 +723,7 @@ __global__ __launch_bounds__(kGradBlock) void k_direct(const T* __restrict__ dy,
     DropKey d{};
     if (DROP) d = drop_key(da);
     float sum[8] = {}, old[8];
-    if (ACC) load_old<T>(grad + (int64_t)mine * s.dim + c, left, old);
+    if (ACC) load_old<T, false>(grad + (int64_t)mine * s.dim + c, left, old);
     while (m0 | m1) {
         uint64_t n0 = m0, n1 = m1;                    // the same tokens once more, for their masks
         RowPiece<T> r[kGradUnroll];
@@ -714,7 +733,7 @@ __global__ __launch_bounds__(kGradBlock) void k_direct(const T* __restrict__ dy,
             at[u] = -1;
             if (m0) { at[u] = __builtin_ctzll(m0); m0 &= m0 - 1; }
             else if (m1) { at[u] = 64 + __builtin_ctzll(m1); m1 &= m1 - 1; }
-            if (at[u] >= 0) r[u] = load_row(dy + (int64_t)at[u] * s.dim + c, left);
+            if (at[u] >= 0) r[u] = load_row<false>(dy + (int64_t)at[u] * s.dim + c, left);
         }
         uint32_t gone[2] = {};
         if (DROP) {
@@ -742,7 +761,7 @@ __global__ __launch_bounds__(kGradBlock) void k_direct(const T* __restrict__ dy,
         sum[j] = sum[j] * c0;
         if (ACC) sum[j] = old[j] + sum[j];
     }
-    store_row<T>(grad + (int64_t)mine * s.dim + c, left, sum);
+    store_row<T, false>(grad + (int64_t)mine * s.dim + c, left, sum);
 }
 
 }  // namespace
