@@ -404,7 +404,7 @@ __global__ __launch_bounds__(kSortBlock) void k_place(SortPass s, const uint32_t
 // part[2c + 1] where it starts in chunk c and part[2c] where it came from an earlier
 // one; k_join adds them in chunk order.
 
-constexpr int kGradBlock = 256, kGradWaves = kGradBlock / 64, kGradCols = 512, kGradUnroll = 8;
+constexpr int kGradBlock = 64, kGradWaves = kGradBlock / 64, kGradCols = 512, kGradUnroll = 4;
 constexpr int kMaxChunk = 32;                         // a wave holds 2 K keys
 
 // A lane's columns of a tile of kGradCols, so that the wave's loads of dy are whole
@@ -420,8 +420,10 @@ __device__ __forceinline__ int64_t piece_col(int p) {
 template <typename T> struct RowPiece;                // a lane's values of one row of dy
 template <> struct RowPiece<uint16_t> { Raw8<uint16_t> r; };
 template <> struct RowPiece<float> { f32x4 a, b; };
-__device__ __forceinline__ f32x4 load4_nt(const float* p) {
-    return __builtin_nontemporal_load(reinterpret_cast<const f32x4_at4*>(p));
+template <bool NT>
+__device__ __forceinline__ f32x4 load4(const float* p) {
+    const f32x4_at4* q = reinterpret_cast<const f32x4_at4*>(p);
+    return NT ? __builtin_nontemporal_load(q) : *q;
 }
 __device__ __forceinline__ f32x4 load4_part(const float* p, int64_t m) {
     return f32x4{m > 0 ? p[0] : 0.0f, m > 1 ? p[1] : 0.0f, m > 2 ? p[2] : 0.0f, m > 3 ? p[3] : 0.0f};
@@ -429,16 +431,16 @@ __device__ __forceinline__ f32x4 load4_part(const float* p, int64_t m) {
 // row: the row's values at the tile's first column; left: columns from there on, and
 // FULL where the tile has them all (most do, and the code for the others, eight times
 // unrolled, would not fit the instruction cache beside it).
-template <bool FULL>
+template <bool FULL, bool NT>
 __device__ __forceinline__ RowPiece<uint16_t> load_row(const uint16_t* row, int64_t left) {
     const int64_t c = piece_col<uint16_t>(0), m = left - c;
-    return {FULL || m >= 8 ? load8<true>(row + c) : load8_part(row + c, (int)(m > 0 ? m : 0))};
+    return {FULL || m >= 8 ? load8<NT>(row + c) : load8_part(row + c, (int)(m > 0 ? m : 0))};
 }
-template <bool FULL>
+template <bool FULL, bool NT>
 __device__ __forceinline__ RowPiece<float> load_row(const float* row, int64_t left) {
     const int64_t c = piece_col<float>(0), d = piece_col<float>(1);
-    return {FULL || left - c >= 4 ? load4_nt(row + c) : load4_part(row + c, left - c),
-            FULL || left - d >= 4 ? load4_nt(row + d) : load4_part(row + d, left - d)};
+    return {FULL || left - c >= 4 ? load4<NT>(row + c) : load4_part(row + c, left - c),
+            FULL || left - d >= 4 ? load4<NT>(row + d) : load4_part(row + d, left - d)};
 }
 __device__ __forceinline__ void widen_row(const RowPiece<uint16_t>& r, float a[8]) { widen(r.r, a); }
 __device__ __forceinline__ void widen_row(const RowPiece<float>& r, float a[8]) {
@@ -465,11 +467,17 @@ __device__ __forceinline__ void load4(const uint16_t* p, float a[4]) {
     const u32x2 w = *reinterpret_cast<const u32x2_at2*>(p);
     a[0] = bf16_lo(w.x); a[1] = bf16_hi(w.x); a[2] = bf16_lo(w.y); a[3] = bf16_hi(w.y);
 }
+template <bool NT>
 __device__ __forceinline__ void store4(float* p, const float a[4]) {
-    *reinterpret_cast<f32x4_at4*>(p) = f32x4{a[0], a[1], a[2], a[3]};
+    f32x4_at4* q = reinterpret_cast<f32x4_at4*>(p);
+    const f32x4 x = {a[0], a[1], a[2], a[3]};
+    if (NT) __builtin_nontemporal_store(x, q); else *q = x;
 }
+template <bool NT>
 __device__ __forceinline__ void store4(uint16_t* p, const float a[4]) {
-    *reinterpret_cast<u32x2_at2*>(p) = u32x2{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
+    u32x2_at2* q = reinterpret_cast<u32x2_at2*>(p);
+    const u32x2 x = {pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
+    if (NT) __builtin_nontemporal_store(x, q); else *q = x;
 }
 // The lane's old values of a row of grad.
 template <typename T, bool FULL, typename G>
@@ -487,16 +495,16 @@ __device__ __forceinline__ void load_old(const G* row, int64_t left, float a[8])
             for (int j = 0; j < 4; ++j) a[4 * h + j] = j < m ? load1(row + c + j) : 0.0f;
     }
 }
-template <typename T, bool FULL, typename G>
+template <typename T, bool FULL, bool NT, typename G>
 __device__ __forceinline__ void store_row(G* row, int64_t left, const float a[8]) {
     if (Cols<T>::kPieces == 1 && (FULL || left - piece_col<T>(0) >= 8)) {
-        store8<false>(row + piece_col<T>(0), a);
+        store8<NT>(row + piece_col<T>(0), a);
         return;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int64_t c = Cols<T>::kPieces == 1 ? piece_col<T>(0) + 4 * h : piece_col<T>(h), m = left - c;
-        if (FULL || m >= 4) store4(row + c, a + 4 * h);
+        if (FULL || m >= 4) store4<NT>(row + c, a + 4 * h);
         else
 #pragma unroll
             for (int j = 0; j < 4; ++j) if (j < m) store1(row + c + j, a[4 * h + j]);
@@ -508,12 +516,13 @@ struct GradShape {
     int64_t n, chunks;
     uint32_t rows;
     int K, tiles;                        // tiles of columns
+    int nt;                              // dy is read nontemporally
 };
 
 // The tokens [first, last) of a wave's chunk: lane l holds token l's key and position.
 struct GradWave { int64_t chunk, c, left; int first, last; bool head_part, tail_part; uint32_t key, pos; };
 
-template <typename T, typename G, bool ACC, bool DROP, bool FULL>
+template <typename T, typename G, bool ACC, bool DROP, bool FULL, bool NT>
 __device__ __forceinline__ void grad_wave(const T* __restrict__ dy, const GradShape& s, GradWave w, float c0,
                                           const DropKey& d, G* __restrict__ grad, float* __restrict__ part) {
     float sum[8] = {};
@@ -528,18 +537,19 @@ __device__ __forceinline__ void grad_wave(const T* __restrict__ dy, const GradSh
             kk[u] = __builtin_amdgcn_readlane(w.key, at);
             const uint32_t p = __builtin_amdgcn_readlane(w.pos, at);
             ends[u] = at + 1 == w.last || (uint32_t)__builtin_amdgcn_readlane(w.key, at + 1) != kk[u];
-            if (t + u < w.last) r[u] = load_row<FULL>(dy + (int64_t)p * s.dim + w.c, w.left);
+            if (t + u < w.last) {
+                const T* row = dy + (int64_t)p * s.dim + w.c;
+                r[u] = load_row<FULL, NT>(row, w.left);
+            }
             if (ACC && t + u < w.last && ends[u])
                 load_old<T, FULL>(grad + (int64_t)kk[u] * s.dim + w.c, w.left, old[u]);
         }
-        uint32_t gone[2] = {};                                       // 8 bits for each u
+        uint32_t gone = 0;                                           // 8 bits for each u
         if (DROP) {
 #pragma unroll 1
             for (int u = 0; u < kGradUnroll && t + u < w.last; ++u) {
                 const uint32_t p = __builtin_amdgcn_readlane(w.pos, t + u);
-                const uint32_t m = dropped_row<T>(d, (uint64_t)p * (uint64_t)s.dim + (uint64_t)w.c) << 8 * (u & 3);
-                gone[0] |= u < 4 ? m : 0;
-                gone[1] |= u < 4 ? 0 : m;
+                gone |= dropped_row<T>(d, (uint64_t)p * (uint64_t)s.dim + (uint64_t)w.c) << 8 * u;
             }
         }
 #pragma unroll
@@ -547,19 +557,19 @@ __device__ __forceinline__ void grad_wave(const T* __restrict__ dy, const GradSh
             if (t + u >= w.last) break;
             float a[8];
             widen_row(r[u], a);
-            if (DROP) drop8(gone[u >> 2] >> 8 * (u & 3), a);
+            if (DROP) drop8(gone >> 8 * u, a);
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum[j] = sum[j] + a[j];
             if (!ends[u]) continue;
             if (w.head_part || (w.tail_part && t + u + 1 == w.last)) {
-                store_row<T, FULL>(part + (2 * w.chunk + (w.head_part ? 0 : 1)) * s.pitch + w.c, s.pitch - w.c, sum);
+                store_row<T, FULL, false>(part + (2 * w.chunk + (w.head_part ? 0 : 1)) * s.pitch + w.c, s.pitch - w.c, sum);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     a[j] = sum[j] * c0;
                     if (ACC) a[j] = old[ACC ? u : 0][j] + a[j];
                 }
-                store_row<T, FULL>(grad + (int64_t)kk[u] * s.dim + w.c, w.left, a);
+                store_row<T, FULL, NT && !ACC>(grad + (int64_t)kk[u] * s.dim + w.c, w.left, a);
             }
             w.head_part = false;
 #pragma unroll
@@ -600,8 +610,9 @@ __global__ __launch_bounds__(kGradBlock) void k_grad(const T* __restrict__ dy, c
     if (w.first >= w.last) return;
     DropKey d{};
     if (DROP) d = drop_key(da);
-    if (w.left >= kGradCols) grad_wave<T, G, ACC, DROP, true>(dy, s, w, c0, d, grad, part);
-    else grad_wave<T, G, ACC, DROP, false>(dy, s, w, c0, d, grad, part);
+    if (w.left < kGradCols) grad_wave<T, G, ACC, DROP, false, false>(dy, s, w, c0, d, grad, part);
+    else if (s.nt) grad_wave<T, G, ACC, DROP, true, true>(dy, s, w, c0, d, grad, part);
+    else grad_wave<T, G, ACC, DROP, true, false>(dy, s, w, c0, d, grad, part);
 }
 
 // Finishes the runs that k_grad left in parts.  A block looks at 64 chunks and takes
@@ -683,7 +694,7 @@ __global__ __launch_bounds__(kJoinBlock) void k_join(const uint32_t* __restrict_
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[j] = o[j] + v[j];
             }
-            store4(p, v);
+            store4<false>(p, v);
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -733,17 +744,15 @@ __global__ __launch_bounds__(kGradBlock) void k_direct(const T* __restrict__ dy,
             at[u] = -1;
             if (m0) { at[u] = __builtin_ctzll(m0); m0 &= m0 - 1; }
             else if (m1) { at[u] = 64 + __builtin_ctzll(m1); m1 &= m1 - 1; }
-            if (at[u] >= 0) r[u] = load_row<false>(dy + (int64_t)at[u] * s.dim + c, left);
+            if (at[u] >= 0) r[u] = load_row<false, false>(dy + (int64_t)at[u] * s.dim + c, left);
         }
-        uint32_t gone[2] = {};
+        uint32_t gone = 0;
         if (DROP) {
 #pragma unroll 1
             for (int u = 0; u < kGradUnroll && (n0 | n1); ++u) {
                 const int p = n0 ? __builtin_ctzll(n0) : 64 + __builtin_ctzll(n1);
                 if (n0) n0 &= n0 - 1; else n1 &= n1 - 1;
-                const uint32_t m = dropped_row<T>(d, (uint64_t)p * (uint64_t)s.dim + (uint64_t)c) << 8 * (u & 3);
-                gone[0] |= u < 4 ? m : 0;
-                gone[1] |= u < 4 ? 0 : m;
+                gone |= dropped_row<T>(d, (uint64_t)p * (uint64_t)s.dim + (uint64_t)c) << 8 * u;
             }
         }
 #pragma unroll
@@ -751,7 +760,7 @@ __global__ __launch_bounds__(kGradBlock) void k_direct(const T* __restrict__ dy,
             if (at[u] < 0) break;
             float a[8];
             widen_row(r[u], a);
-            if (DROP) drop8(gone[u >> 2] >> 8 * (u & 3), a);
+            if (DROP) drop8(gone >> 8 * u, a);
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum[j] = sum[j] + a[j];
         }
@@ -761,7 +770,7 @@ __global__ __launch_bounds__(kGradBlock) void k_direct(const T* __restrict__ dy,
         sum[j] = sum[j] * c0;
         if (ACC) sum[j] = old[j] + sum[j];
     }
-    store_row<T, false>(grad + (int64_t)mine * s.dim + c, left, sum);
+    store_row<T, false, false>(grad + (int64_t)mine * s.dim + c, left, sum);
 }
 
 }  // namespace

@@ -269,6 +269,7 @@ extern "C" int gsz_embedding_grad(const void* ids, int32_t id_type, int64_t n, c
     g.K = chunk_for(n, dim);
     g.chunks = (n + g.K - 1) / g.K;
     g.tiles = col_tiles(dim);
+    g.nt = n * dim * ds >= (int64_t)64 << 20;
     const bool direct = n <= kDirectMax, rank = !direct && n <= kRankMax, f32 = grad_type == GSZ_TYPE_F32;
     // Rows that a block clears: about 128 KiB beside the sort's or the sums' blocks,
     // 256 KiB in whole words of 64 rows for the rank sort's, which hold every key.
