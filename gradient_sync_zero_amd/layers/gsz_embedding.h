@@ -615,11 +615,11 @@ __global__ __launch_bounds__(kGradBlock) void k_grad(const T* __restrict__ dy, c
     else grad_wave<T, G, ACC, DROP, true, false>(dy, s, w, c0, d, grad, part);
 }
 
-// Finishes the runs that k_grad left in parts.  A block looks at 64 chunks and takes
+// Finishes the runs that k_grad left in parts.  A block looks at kJoinChunks chunks and takes
 // kJoinCols columns of the runs that start in one of them and leave a tail part: a run
 // of at most kJoinWaves parts is one wave's, a longer one the block's, each wave
 // summing a stretch of its parts and the first wave those sums, all in order.
-constexpr int kJoinBlock = 1024, kJoinWaves = kJoinBlock / 64, kJoinCols = 256;
+constexpr int kJoinBlock = 512, kJoinWaves = kJoinBlock / 64, kJoinCols = 256, kJoinChunks = 32;
 // a + part rows [k, end) of the run that starts in `chunk`, at the lane's columns.
 __device__ __forceinline__ f32x4 sum_parts(const float* __restrict__ part, int64_t pitch, int64_t chunk,
                                            int64_t k, int64_t end) {
@@ -643,7 +643,7 @@ __global__ __launch_bounds__(kJoinBlock) void k_join(const uint32_t* __restrict_
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t g = (int64_t)blockIdx.x / tiles, c0l = ((int64_t)blockIdx.x % tiles) * kJoinCols;
     const int64_t c = c0l + 4 * lane, cp = c < s.pitch ? c : 0;        // lanes past the row read its start
-    const int64_t mine = g * 64 + lane, e = (mine + 1) * s.K;        // this lane's chunk and its end
+    const int64_t mine = g * kJoinChunks + lane, e = (mine + 1) * s.K;        // this lane's chunk and its end
     uint32_t k = s.rows;
     bool starts = false, inside = false;                             // a run starts here, or comes from before;
     if (mine < s.chunks && e < s.n) {                                // either way it goes on into the next chunk
@@ -651,7 +651,7 @@ __global__ __launch_bounds__(kJoinBlock) void k_join(const uint32_t* __restrict_
         const uint32_t next = key[e], before = mine > 0 ? key[e - s.K - 1] : 0xFFFFFFFFu;
         const uint32_t past = e + s.K < s.n ? key[e + s.K] : 0xFFFFFFFFu;
         const bool on = k != s.rows && k == next;
-        starts = on && k != before && k == past;
+        starts = lane < kJoinChunks && on && k != before && k == past;
         inside = on && k == before;
     }
     const uint64_t through = __ballot(inside);
@@ -659,7 +659,7 @@ __global__ __launch_bounds__(kJoinBlock) void k_join(const uint32_t* __restrict_
     for (uint64_t m = __ballot(starts); m; m &= m - 1, ++order) {
         const int l = __builtin_ctzll(m);
         const uint32_t row = __builtin_amdgcn_readlane(k, l);
-        const int64_t chunk = g * 64 + l;
+        const int64_t chunk = g * kJoinChunks + l;
         // The chunks of the run: this one, those that it passes through, its last.
         const uint64_t ends = l < 63 ? ~through >> (l + 1) << (l + 1) : 0;
         int64_t parts = (ends ? __builtin_ctzll(ends) : 64) - l + 1;
