@@ -111,11 +111,12 @@ __global__ __launch_bounds__(kLookBlock) void k_lookup(const T* __restrict__ tab
 // that: the blocks that clear ride along with the sort, whose few blocks leave
 // the memory idle.
 
-// Clears the rows r0 + i, i a set bit of `missing`, with the whole block: neighbours
+// Clears the rows r0 + i, i a set bit of `missing`, with `threads` threads: neighbours
 // as one stretch of memory in whole 16-byte vectors, whatever the rows' alignment (row by
 // row at the rows' own places, 31,000 rows of 4097 fp32 took 210 us, 2.5 TB/s).
 template <typename G>
-__device__ __forceinline__ void clear_rows(G* __restrict__ grad, int64_t dim, int64_t r0, uint64_t missing) {
+__device__ __forceinline__ void clear_rows(G* __restrict__ grad, int64_t dim, int64_t r0, uint64_t missing,
+                                           int thread, int threads) {
     while (missing) {
         const int first = __builtin_ctzll(missing);
         const uint64_t rest = ~(missing >> first);
@@ -127,13 +128,15 @@ __device__ __forceinline__ void clear_rows(G* __restrict__ grad, int64_t dim, in
         if (head > n) head = n;
         const int64_t vecs = (n - head) * (int64_t)sizeof(G) / 16;
         u32x4* q = reinterpret_cast<u32x4*>(p + head);
-        for (int64_t i = threadIdx.x; i < vecs; i += blockDim.x)
+        for (int64_t i = thread; i < vecs; i += threads)
             __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, q + i);
         const int64_t tail = head + vecs * (16 / (int64_t)sizeof(G));
-        if ((int64_t)threadIdx.x < head) p[threadIdx.x] = 0;
-        if ((int64_t)threadIdx.x < n - tail) p[tail + threadIdx.x] = 0;
+        if (thread < head) p[thread] = 0;
+        if (thread < n - tail) p[tail + thread] = 0;
     }
 }
+
+constexpr int kSortBlock = 256;                       // of the launches that clear beside the sort
 
 // Which part of the table a launch clears: `per` rows (at most 64) for each of its
 // blocks from `first_block` on, rows [row0, row1).
@@ -153,8 +156,8 @@ __device__ __forceinline__ void clear_block(const ClearShape& c, const Ids& ids,
         missing = !(i < (uint64_t)n && row_of(ids, i) == (uint32_t)v);
     }
     const uint64_t m = __ballot(missing);
-    if (c.f32) clear_rows(static_cast<float*>(c.grad), c.dim, r0, m);
-    else clear_rows(static_cast<uint16_t*>(c.grad), c.dim, r0, m);
+    if (c.f32) clear_rows(static_cast<float*>(c.grad), c.dim, r0, m, threadIdx.x, kSortBlock);
+    else clear_rows(static_cast<uint16_t*>(c.grad), c.dim, r0, m, threadIdx.x, kSortBlock);
 }
 
 // ------------------------------------------------------------------ sort --
@@ -194,6 +197,26 @@ __global__ __launch_bounds__(kRankBlock) void k_rank(Ids ids, int n, uint32_t* _
     }
     if (tid < 128) seen[tid >> 1][tid & 1] = 0;
     __syncthreads();
+    // The stores that clear leave first and land while the block compares keys.  Each wave
+    // has a sixteenth of the block's rows (clear.per is a power of two).
+    if (clear.grad) {
+        const int64_t r0 = (int64_t)blockIdx.x * clear.per * 64;
+        for (int j = tid; j < n; j += kRankBlock) {
+            const int64_t v = (int64_t)(PACKED ? all[j] >> kRankBits : all[j]) - r0;
+            if (v >= 0 && v < (int64_t)clear.per * 64) atomicOr(&seen[v >> 6][v >> 5 & 1], 1u << (v & 31));
+        }
+        __syncthreads();
+        const int share = clear.per * 64 / (kRankBlock / 64), first = (tid >> 6) * share;
+        for (int at = first; at < first + share; at += 64) {
+            const int64_t r = r0 + at, left = clear.row1 - r;
+            if (left <= 0) break;
+            uint64_t m = ~((uint64_t)seen[at >> 6][1] << 32 | seen[at >> 6][0]) >> (at & 63);
+            const int64_t most = left < share ? left : share;
+            if (most < 64) m &= ((uint64_t)1 << most) - 1;
+            if (clear.f32) clear_rows(static_cast<float*>(clear.grad), clear.dim, r, m, tid & 63, 64);
+            else clear_rows(static_cast<uint16_t*>(clear.grad), clear.dim, r, m, tid & 63, 64);
+        }
+    }
     const int t = tid % kRankTokens, slice = tid / kRankTokens;
     const int i = blockIdx.x * kRankTokens + t;
     if ((int64_t)blockIdx.x * kRankTokens < n) {
@@ -226,22 +249,6 @@ __global__ __launch_bounds__(kRankBlock) void k_rank(Ids ids, int n, uint32_t* _
             pos[s] = (uint32_t)i;
         }
     }
-    if (!clear.grad) return;
-    // seen: 64 words of 64 rows each
-    const int64_t r0 = (int64_t)blockIdx.x * clear.per * 64;
-    for (int j = tid; j < n; j += kRankBlock) {
-        const int64_t v = (int64_t)(PACKED ? all[j] >> kRankBits : all[j]) - r0;
-        if (v >= 0 && v < (int64_t)clear.per * 64) atomicOr(&seen[v >> 6][v >> 5 & 1], 1u << (v & 31));
-    }
-    __syncthreads();
-    for (int w = 0; w < clear.per; ++w) {
-        const int64_t r = r0 + 64 * w, count = clear.row1 - r;
-        if (count <= 0) break;
-        uint64_t m = ~((uint64_t)seen[w][1] << 32 | seen[w][0]);
-        if (count < 64) m &= ((uint64_t)1 << count) - 1;
-        if (clear.f32) clear_rows(static_cast<float*>(clear.grad), clear.dim, r, m);
-        else clear_rows(static_cast<uint16_t*>(clear.grad), clear.dim, r, m);
-    }
 }
 
 // More tokens: stable counting passes over digits of the key, lowest first, a launch
@@ -249,7 +256,7 @@ __global__ __launch_bounds__(kRankBlock) void k_rank(Ids ids, int n, uint32_t* _
 // tile of `rounds` times kSortTile tokens.  (Counting the next digit while placing this
 // one, with an atomic per token where it lands, saved a launch and cost 10 us of
 // atomics on 16 Ki tokens.)
-constexpr int kSortBlock = 256, kSortWaves = kSortBlock / 64, kSortMaxBins = 1024;
+constexpr int kSortWaves = kSortBlock / 64, kSortMaxBins = 1024;
 constexpr int kSortPer = 4, kSortTile = kSortBlock * kSortPer;
 constexpr int kSortBinsPer = kSortMaxBins / kSortBlock;
 struct SortPass {
@@ -721,7 +728,7 @@ __global__ __launch_bounds__(kGradBlock) void k_direct(const T* __restrict__ dy,
             if ((uint32_t)__builtin_amdgcn_readlane(k0, j) == (uint64_t)v) missing = false;
             if ((uint32_t)__builtin_amdgcn_readlane(k1, j) == (uint64_t)v) missing = false;
         }
-        clear_rows(grad, s.dim, r0, __ballot(missing));
+        clear_rows(grad, s.dim, r0, __ballot(missing), threadIdx.x, kGradBlock);
         return;
     }
     const int64_t w = (int64_t)blockIdx.x * kGradWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

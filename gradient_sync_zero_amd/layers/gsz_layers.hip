@@ -276,7 +276,8 @@ extern "C" int gsz_embedding_grad(const void* ids, int32_t id_type, int64_t n, c
     // 256 KiB in whole words of 64 rows for the rank sort's, which hold every key.
     const int64_t row_bytes = dim * gs;
     auto clamp = [](int64_t v, int64_t most) { return (int)(v < 1 ? 1 : v > most ? most : v); };
-    const int per = rank ? clamp(((int64_t)256 << 10) / (64 * row_bytes), 64) : clamp(((int64_t)32 << 10) / row_bytes, 64);
+    int per = rank ? clamp(((int64_t)256 << 10) / (64 * row_bytes), 64) : clamp(((int64_t)32 << 10) / row_bytes, 64);
+    while (rank && per & (per - 1)) per &= per - 1;                  // a power of two
     const int64_t clear_blocks = accumulate ? 0 : (rows + (int64_t)per * (rank ? 64 : 1) - 1) / ((int64_t)per * (rank ? 64 : 1));
     const int64_t sum_blocks = ((direct ? n : g.chunks) * g.tiles + kGradWaves - 1) / kGradWaves;
     const int join_tiles = (int)((dim + kJoinCols - 1) / kJoinCols);
