@@ -411,112 +411,8 @@ __global__ __launch_bounds__(kSortBlock) void k_place(SortPass s, const uint32_t
 // part[2c + 1] where it starts in chunk c and part[2c] where it came from an earlier
 // one; k_join adds them in chunk order.
 
-constexpr int kGradBlock = 64, kGradWaves = kGradBlock / 64, kGradCols = 512, kGradUnroll = 4;
+constexpr int kGradBlock = 64, kGradWaves = kGradBlock / 64, kGradCols = kTile, kGradUnroll = 4;
 constexpr int kMaxChunk = 32;                         // a wave holds 2 K keys
-
-// A lane's columns of a tile of kGradCols, so that the wave's loads of dy are whole
-// lines: 8 in a row for bf16 (16 bytes), two groups of 4 for fp32.
-template <typename T> struct Cols;
-template <> struct Cols<uint16_t> { static constexpr int kPieces = 1, kWidth = 8; };
-template <> struct Cols<float> { static constexpr int kPieces = 2, kWidth = 4; };
-template <typename T>
-__device__ __forceinline__ int64_t piece_col(int p) {
-    return p * 64 * Cols<T>::kWidth + Cols<T>::kWidth * (threadIdx.x & 63);
-}
-
-template <typename T> struct RowPiece;                // a lane's values of one row of dy
-template <> struct RowPiece<uint16_t> { Raw8<uint16_t> r; };
-template <> struct RowPiece<float> { f32x4 a, b; };
-template <bool NT>
-__device__ __forceinline__ f32x4 load4(const float* p) {
-    const f32x4_at4* q = reinterpret_cast<const f32x4_at4*>(p);
-    return NT ? __builtin_nontemporal_load(q) : *q;
-}
-__device__ __forceinline__ f32x4 load4_part(const float* p, int64_t m) {
-    return f32x4{m > 0 ? p[0] : 0.0f, m > 1 ? p[1] : 0.0f, m > 2 ? p[2] : 0.0f, m > 3 ? p[3] : 0.0f};
-}
-// row: the row's values at the tile's first column; left: columns from there on, and
-// FULL where the tile has them all (most do, and the code for the others, eight times
-// unrolled, would not fit the instruction cache beside it).
-template <bool FULL, bool NT>
-__device__ __forceinline__ RowPiece<uint16_t> load_row(const uint16_t* row, int64_t left) {
-    const int64_t c = piece_col<uint16_t>(0), m = left - c;
-    return {FULL || m >= 8 ? load8<NT>(row + c) : load8_part(row + c, (int)(m > 0 ? m : 0))};
-}
-template <bool FULL, bool NT>
-__device__ __forceinline__ RowPiece<float> load_row(const float* row, int64_t left) {
-    const int64_t c = piece_col<float>(0), d = piece_col<float>(1);
-    return {FULL || left - c >= 4 ? load4<NT>(row + c) : load4_part(row + c, left - c),
-            FULL || left - d >= 4 ? load4<NT>(row + d) : load4_part(row + d, left - d)};
-}
-__device__ __forceinline__ void widen_row(const RowPiece<uint16_t>& r, float a[8]) { widen(r.r, a); }
-__device__ __forceinline__ void widen_row(const RowPiece<float>& r, float a[8]) {
-    widen(Raw8<float>{r.a, r.b}, a);
-}
-// The lane's values zeroed where dropped; first: element index of the tile's first column.
-// Each lane draws the mask of 8 columns in a row; fp32's groups of 4 fetch theirs.
-template <typename T>
-__device__ __forceinline__ uint32_t dropped_row(const DropKey& d, uint64_t first) {
-    const int lane = threadIdx.x & 63;
-    const uint32_t m = dropped8(d, first + 8 * lane);
-    if (Cols<T>::kPieces == 1) return m;
-    const uint32_t lo = (uint32_t)__shfl((int)m, lane >> 1) >> 4 * (lane & 1);
-    const uint32_t hi = (uint32_t)__shfl((int)m, 32 + (lane >> 1)) >> 4 * (lane & 1);
-    return (lo & 15) | (hi & 15) << 4;
-}
-
-// Groups of 4 values of either type (grad and partial rows, at any element).
-__device__ __forceinline__ void load4(const float* p, float a[4]) {
-    const f32x4 x = *reinterpret_cast<const f32x4_at4*>(p);
-    a[0] = x.x; a[1] = x.y; a[2] = x.z; a[3] = x.w;
-}
-__device__ __forceinline__ void load4(const uint16_t* p, float a[4]) {
-    const u32x2 w = *reinterpret_cast<const u32x2_at2*>(p);
-    a[0] = bf16_lo(w.x); a[1] = bf16_hi(w.x); a[2] = bf16_lo(w.y); a[3] = bf16_hi(w.y);
-}
-template <bool NT>
-__device__ __forceinline__ void store4(float* p, const float a[4]) {
-    f32x4_at4* q = reinterpret_cast<f32x4_at4*>(p);
-    const f32x4 x = {a[0], a[1], a[2], a[3]};
-    if (NT) __builtin_nontemporal_store(x, q); else *q = x;
-}
-template <bool NT>
-__device__ __forceinline__ void store4(uint16_t* p, const float a[4]) {
-    u32x2_at2* q = reinterpret_cast<u32x2_at2*>(p);
-    const u32x2 x = {pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
-    if (NT) __builtin_nontemporal_store(x, q); else *q = x;
-}
-// The lane's old values of a row of grad.
-template <typename T, bool FULL, typename G>
-__device__ __forceinline__ void load_old(const G* row, int64_t left, float a[8]) {
-    if (Cols<T>::kPieces == 1 && (FULL || left - piece_col<T>(0) >= 8)) {
-        widen(load8<false>(row + piece_col<T>(0)), a);
-        return;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int64_t c = Cols<T>::kPieces == 1 ? piece_col<T>(0) + 4 * h : piece_col<T>(h), m = left - c;
-        if (FULL || m >= 4) load4(row + c, a + 4 * h);
-        else
-#pragma unroll
-            for (int j = 0; j < 4; ++j) a[4 * h + j] = j < m ? load1(row + c + j) : 0.0f;
-    }
-}
-template <typename T, bool FULL, bool NT, typename G>
-__device__ __forceinline__ void store_row(G* row, int64_t left, const float a[8]) {
-    if (Cols<T>::kPieces == 1 && (FULL || left - piece_col<T>(0) >= 8)) {
-        store8<NT>(row + piece_col<T>(0), a);
-        return;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int64_t c = Cols<T>::kPieces == 1 ? piece_col<T>(0) + 4 * h : piece_col<T>(h), m = left - c;
-        if (FULL || m >= 4) store4<NT>(row + c, a + 4 * h);
-        else
-#pragma unroll
-            for (int j = 0; j < 4; ++j) if (j < m) store1(row + c + j, a[4 * h + j]);
-    }
-}
 
 struct GradShape {
     int64_t dim, pitch;                  // pitch: floats of a partial row, a multiple of 8

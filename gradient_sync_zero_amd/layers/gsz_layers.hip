@@ -109,7 +109,7 @@ int col_tiles(int64_t dim) { return (int)((dim + kGradCols - 1) / kGradCols); }
 
 int chunk_for(int64_t n, int64_t dim) {
     int K = kMaxChunk;
-    while (K > 8 && (n + K - 1) / K * col_tiles(dim) < 4096) K /= 2;
+    while (K > 4 && (n + K - 1) / K * col_tiles(dim) < 4096) K /= 2;
     return K;
 }
 
@@ -160,7 +160,7 @@ extern "C" int gsz_dropout(const void* x, const void* add, void* y, int64_t n, i
     if (off_by(x, size) || off_by(y, size) || off_by(add, size)) { set_error("%s: a buffer is not aligned to its values", who); return GSZ_ERR_MISALIGNED; }
     if ((rc = check_device(who))) return rc;
     if (n == 0) return GSZ_OK;
-    const int grid = grid_for((n + 8 * kDropBlock - 1) / (8 * kDropBlock), kDropBlock);
+    const int grid = grid_for((n + kDropTile - 1) / kDropTile, kDropBlock);
     with_type(type, [&](auto t) {
         using T = decltype(t);
         with_bool(add != nullptr, [&](auto a) {
