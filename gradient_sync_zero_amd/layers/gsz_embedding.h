@@ -136,7 +136,7 @@ __device__ __forceinline__ void clear_rows(G* __restrict__ grad, int64_t dim, in
     }
 }
 
-constexpr int kSortBlock = 256;                       // of the launches that clear beside the sort
+constexpr int kSortBlock = 512;                       // of the launches that clear beside the sort
 
 // Which part of the table a launch clears: `per` rows (at most 64) for each of its
 // blocks from `first_block` on, rows [row0, row1).
@@ -257,7 +257,7 @@ __global__ __launch_bounds__(kRankBlock) void k_rank(Ids ids, int n, uint32_t* _
 // one, with an atomic per token where it lands, saved a launch and cost 10 us of
 // atomics on 16 Ki tokens.)
 constexpr int kSortWaves = kSortBlock / 64, kSortMaxBins = 1024;
-constexpr int kSortPer = 4, kSortTile = kSortBlock * kSortPer;
+constexpr int kSortPer = 1, kSortTile = kSortBlock * kSortPer;
 constexpr int kSortBinsPer = kSortMaxBins / kSortBlock;
 struct SortPass {
     Ids ids;                              // the tokens themselves (FIRST),
