@@ -611,7 +611,7 @@ __global__ __launch_bounds__(kJoinBlock) void k_join(const uint32_t* __restrict_
 // n <= kDirectMax tokens in one launch without a sort: the wave of (token, tile of
 // columns) ends if its row came earlier, else it sums the tokens of its row in order.
 // Blocks from clear.first_block on clear the rows that no token has.
-constexpr int kDirectMax = 128;
+constexpr int kDirectMax = 128, kDirectUnroll = 8;
 template <typename T, typename G, bool ACC, bool DROP>
 __global__ __launch_bounds__(kGradBlock) void k_direct(const T* __restrict__ dy, Ids ids, GradShape s, float c0,
                                                        DropArgs da, G* __restrict__ grad, ClearShape clear) {
@@ -640,30 +640,30 @@ __global__ __launch_bounds__(kGradBlock) void k_direct(const T* __restrict__ dy,
     if (ACC) load_old<T, false>(grad + (int64_t)mine * s.dim + c, left, old);
     while (m0 | m1) {
         uint64_t n0 = m0, n1 = m1;                    // the same tokens once more, for their masks
-        RowPiece<T> r[kGradUnroll];
-        int at[kGradUnroll];
+        RowPiece<T> r[kDirectUnroll];
+        int at[kDirectUnroll];
 #pragma unroll
-        for (int u = 0; u < kGradUnroll; ++u) {
+        for (int u = 0; u < kDirectUnroll; ++u) {
             at[u] = -1;
             if (m0) { at[u] = __builtin_ctzll(m0); m0 &= m0 - 1; }
             else if (m1) { at[u] = 64 + __builtin_ctzll(m1); m1 &= m1 - 1; }
             if (at[u] >= 0) r[u] = load_row<false, false>(dy + (int64_t)at[u] * s.dim + c, left);
         }
-        uint32_t gone = 0;
+        uint64_t gone = 0;
         if (DROP) {
 #pragma unroll 1
-            for (int u = 0; u < kGradUnroll && (n0 | n1); ++u) {
+            for (int u = 0; u < kDirectUnroll && (n0 | n1); ++u) {
                 const int p = n0 ? __builtin_ctzll(n0) : 64 + __builtin_ctzll(n1);
                 if (n0) n0 &= n0 - 1; else n1 &= n1 - 1;
-                gone |= dropped_row<T>(d, (uint64_t)p * (uint64_t)s.dim + (uint64_t)c) << 8 * u;
+                gone |= (uint64_t)dropped_row<T>(d, (uint64_t)p * (uint64_t)s.dim + (uint64_t)c) << 8 * u;
             }
         }
 #pragma unroll
-        for (int u = 0; u < kGradUnroll; ++u) {
+        for (int u = 0; u < kDirectUnroll; ++u) {
             if (at[u] < 0) break;
             float a[8];
             widen_row(r[u], a);
-            if (DROP) drop8(gone >> 8 * u, a);
+            if (DROP) drop8((uint32_t)(gone >> 8 * u), a);
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum[j] = sum[j] + a[j];
         }
