@@ -565,55 +565,65 @@ def adamw_step(master, m, v, g, coef, hp, out_bf16, stream=None):
                                  _ptr(out_bf16, "out_bf16", bt, min_numel=n), _stream(stream)))
 
 
-_TYPES = {}          # dtype -> (GSZ_TYPE_*, bytes); filled on first use
+# The checks of the layer calls below cost host time that a launch of a few
+# microseconds shows, so each tensor is looked at once.
+_VALUES, _IDS, _RNG = {}, {}, {}                 # dtype -> GSZ_TYPE_*; filled on first use
 
 
-def _types():
+def _fill_types():
     import torch
-    if not _TYPES:
-        _TYPES.update({torch.bfloat16: (0, 2), torch.uint16: (0, 2), torch.int16: (0, 2),
-                       torch.float32: (1, 4), torch.int32: (2, 4), torch.int64: (3, 8)})
-    return _TYPES
+    globals()["_getDevice"] = torch._C._cuda_getDevice
+    globals()["_getRawStream"] = torch._C._cuda_getCurrentRawStream
+    _IDS.update({torch.int32: 2, torch.int64: 3})
+    _RNG.update({torch.int64: 3, torch.uint64: 3})
+    # last: a call of another thread that finds this filled finds all filled
+    _VALUES.update({torch.bfloat16: 0, torch.uint16: 0, torch.int16: 0, torch.float32: 1})
 
 
-def _typed(t, name, ids=False, numel=None):
-    """(GSZ_TYPE_*, address) of a value tensor (bf16 or its bits, or fp32) or, with
-    ids, of an id tensor (int32 or int64), checked as _ptr does."""
+def _arg(t, name, types, what, numel=None, dev=None):
+    """(GSZ_TYPE_*, address, device) of a contiguous device tensor, on device `dev`
+    if given, of one of `types` and of numel elements if given."""
     if t is None:
         raise ValueError(f"{name} is required")
-    vt = _types().get(t.dtype, (-1,))[0]
-    if vt < 0 or (vt >= 2) != ids:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected "
-                         + ("int32 or int64" if ids else "bf16 (or its bits) or float32"))
-    return vt, _ptr(t, name, (t.dtype,), numel=numel)
+    ty = types.get(t.dtype, -1)
+    if ty < 0:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {what}")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} has {t.numel()} elements, the call needs exactly {numel}")
+    where = t.get_device()
+    if where < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    if dev is not None and where != dev:
+        raise ValueError(f"{name} is on cuda:{where}, another tensor of the call on cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return ty, t.data_ptr(), where
 
 
-def _same_type(t, name, x, numel):
-    """Address of t (or None), of x's dtype and numel elements."""
-    return _ptr(t, name, (x.dtype,), allow_none=True, numel=numel)
+_V, _I, _R = "bf16 (or its bits) or float32", "int32 or int64", "int64"
 
 
-def _rng_site(rng, site):
+def _value(t, name, numel=None, dev=None):
+    return _arg(t, name, _VALUES, _V, numel, dev)
+
+
+def _rng_site(rng, site, dev):
     """Address of {seed, step}, two 64-bit integers on the device, and the site."""
-    import torch
     if not 0 <= site < 1 << 32:
         raise ValueError(f"site {site} is not a 32-bit number")
-    return _ptr(rng, "rng", (torch.int64, torch.uint64), allow_none=True, numel=2), site
+    return None if rng is None else _arg(rng, "rng", _RNG, _R, 2, dev)[1]
 
 
-def _layer_stream(stream, *tensors):
-    """The stream of a call whose kernels run on the current device: every tensor,
-    and the stream if given as an object, must be there."""
-    import torch
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+def _layer_stream(stream, dev):
+    """The stream of a call whose tensors are on device dev: the kernels run on the
+    current device, which must be that one, and the stream there too."""
+    if _getDevice() != dev:
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{_getDevice()}")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _getRawStream(dev)
     where = getattr(stream, "device", None)
     if where is not None and where.index != dev:
-        raise ValueError(f"stream is on {where}, the current device is cuda:{dev}")
+        raise ValueError(f"stream is on {where}, the tensors are on cuda:{dev}")
     return _stream(stream)
 
 
@@ -621,12 +631,17 @@ def dropout(x, y, p, rng, site=0, add=None, stream=None):
     """gsz_dropout: y = (add or 0) + dropout(x) with probability p.  rng: a device
     tensor of two int64, {seed, step}.  The backward pass is the same call on the
     gradient."""
-    n = x.numel()
-    vt, xp = _typed(x, "x")
-    yp = _ptr(y, "y", (x.dtype,), numel=n)
-    ap = _same_type(add, "add", x, n)
-    rp, site = _rng_site(rng, site)
-    _check(load().gsz_dropout(xp, ap, yp, n, vt, p, rp, site, _layer_stream(stream, x, y, add, rng)))
+    if not _VALUES:
+        _fill_types()
+    vt, xp, dev = _value(x, "x")
+    n, same, what = x.numel(), {x.dtype: vt}, "x's"
+    yp = _arg(y, "y", same, what, n, dev)[1]
+    ap = None if add is None else _arg(add, "add", same, what, n, dev)[1]
+    rp = _rng_site(rng, site, dev)
+    lib = load()
+    rc = lib.gsz_dropout(xp, ap, yp, n, vt, p, rp, site, _layer_stream(stream, dev))
+    if rc:
+        _check(rc, lib)
 
 
 def _table_shape(table, name):
@@ -639,14 +654,19 @@ def embedding_lookup(ids, table, out, scale=1.0, p=0.0, rng=None, site=0, stream
     """gsz_embedding_lookup: out[i] = dropout(scale * table[ids[i]]), a zero row where
     ids[i] is outside the table.  table is 2-D (rows, dim), for instance
     plan.view(t, gathered).view(rows, dim); out holds ids.numel() * dim values."""
+    if not _VALUES:
+        _fill_types()
     rows, dim = _table_shape(table, "table")
-    it, ip = _typed(ids, "ids", ids=True)
+    tt, tp, dev = _value(table, "table")
+    it, ip, _ = _arg(ids, "ids", _IDS, _I, None, dev)
     n = ids.numel()
-    tt, tp = _typed(table, "table")
-    ot, op = _typed(out, "out", numel=n * dim)
-    rp, site = _rng_site(rng, site)
-    _check(load().gsz_embedding_lookup(tp, tt, rows, dim, ip, it, n, scale, p, rp, site, op, ot,
-                                       _layer_stream(stream, ids, table, out, rng)))
+    ot, op, _ = _value(out, "out", n * dim, dev)
+    rp = _rng_site(rng, site, dev)
+    lib = load()
+    rc = lib.gsz_embedding_lookup(tp, tt, rows, dim, ip, it, n, scale, p, rp, site, op, ot,
+                                  _layer_stream(stream, dev))
+    if rc:
+        _check(rc, lib)
 
 
 def embedding_workspace_bytes(n, rows, dim):
@@ -662,15 +682,20 @@ def embedding_grad(ids, dy, grad, ws, scale=1.0, p=0.0, rng=None, site=0, accumu
     plan.view(t, flat).view(rows, dim) of a bf16 or fp32 bucket buffer) or, with
     accumulate, added to it.  ws: a tensor of at least embedding_workspace_bytes (None
     where that is 0)."""
+    if not _VALUES:
+        _fill_types()
     rows, dim = _table_shape(grad, "grad")
-    it, ip = _typed(ids, "ids", ids=True)
+    gt, gp, dev = _value(grad, "grad")
+    it, ip, _ = _arg(ids, "ids", _IDS, _I, None, dev)
     n = ids.numel()
-    dt, dp = _typed(dy, "dy", numel=n * dim)
-    gt, gp = _typed(grad, "grad")
+    dt, dp, _ = _value(dy, "dy", n * dim, dev)
     wp, nbytes = None, 0
     if ws is not None:
-        wp, nbytes = _ptr(ws, "ws", (ws.dtype,)), ws.numel() * ws.element_size()
-    rp, site = _rng_site(rng, site)
-    _check(load().gsz_embedding_grad(ip, it, n, dp, dt, rows, dim, scale, p, rp, site, gp, gt,
-                                     1 if accumulate else 0, wp, nbytes,
-                                     _layer_stream(stream, ids, dy, grad, ws, rng)))
+        wp = _arg(ws, "ws", {ws.dtype: 0}, "", None, dev)[1]
+        nbytes = ws.numel() * ws.element_size()
+    rp = _rng_site(rng, site, dev)
+    lib = load()
+    rc = lib.gsz_embedding_grad(ip, it, n, dp, dt, rows, dim, scale, p, rp, site, gp, gt,
+                                1 if accumulate else 0, wp, nbytes, _layer_stream(stream, dev))
+    if rc:
+        _check(rc, lib)

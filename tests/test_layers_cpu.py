@@ -72,9 +72,9 @@ def test_workspace_bytes():
                          (300_000, 5, 4), (1 << 22, 1 << 30, 1)):
         b = G.embedding_workspace_bytes(n, rows, dim)
         # none for up to 128 tokens; else sorted pairs twice, a digit table, a token of
-        # each row, two fp32 partial rows per chunk of at least 8 tokens
+        # each row, two fp32 partial rows per chunk of at least 4 tokens
         assert b % 256 == 0 and (b >= 8 * n if n > 128 else b == 0)
-        assert b <= 16 * n + 4 * 256 * 1024 + 4 * rows + 8 * (-(-n // 8)) * (dim + 7) + 4096
+        assert b <= 16 * n + 4 * 256 * 1024 + 4 * rows + 8 * (-(-n // 4)) * (dim + 7) + 4096
     for bad in ((-1, 1, 1), (1, -1, 1), (1, 1, -1), (1 << 31, 1, 1), (1, 1 << 31, 1), (1, 1, 1 << 30)):
         with pytest.raises(G.GszError):
             G.embedding_workspace_bytes(*bad)
@@ -117,6 +117,9 @@ class Dev:
 
     def element_size(self):
         return 4
+
+    def get_device(self):
+        return 0
 
     def is_contiguous(self):
         return True
