@@ -236,6 +236,12 @@ __device__ __forceinline__ void drop_numbers(const DropKey& d, uint64_t block, u
     }
 }
 
+// a[j] <- 0 where element first + j is dropped (chosen, not multiplied: an infinity or
+// NaN in a dropped place leaves 0), first a multiple of 8.
+__device__ __forceinline__ void drop8_at(const DropKey& d, const uint32_t u[8], float a[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = u[j] < d.threshold ? 0.0f : a[j];
+}
 // Bit j: element first + j is dropped.
 __device__ __forceinline__ uint32_t dropped8(const DropKey& d, uint64_t first) {
     uint32_t u[8], m = 0;
@@ -251,8 +257,7 @@ __device__ __forceinline__ uint32_t dropped8(const DropKey& d, uint64_t first) {
     }
     return m;
 }
-// a[j] <- 0 where bit j is set (chosen, not multiplied: an infinity or NaN in a
-// dropped place leaves 0).
+// a[j] <- 0 where bit j is set.
 __device__ __forceinline__ void drop8(uint32_t gone, float a[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) a[j] = (gone >> j & 1) ? 0.0f : a[j];
@@ -283,14 +288,18 @@ __device__ __forceinline__ void dropout_tile(const T* x, const T* add, T* y, int
     RowPiece<T> q{};
     if (ADD) q = load_row<FULL, true>(add + e, left);
     // The mask needs no data: it is drawn while the loads are on their way.
-    uint32_t gone = 0;
-    if (DROP) gone = dropped_row<T>(d, (uint64_t)e);
+    // (bf16's lanes use the numbers themselves, which saves packing and unpacking bits.)
+    constexpr bool kBits = Cols<T>::kPieces > 1;
+    uint32_t gone = 0, u[8];
+    if (DROP && kBits) gone = dropped_row<T>(d, (uint64_t)e);
+    if (DROP && !kBits) drop_numbers(d, ((uint64_t)e >> 3) + (threadIdx.x & 63), u);
     float a[8], b[8];
     widen_row(r, a);
     if (ADD) widen_row(q, b);
 #pragma unroll
     for (int j = 0; j < 8; ++j) a[j] = a[j] * k;
-    if (DROP) drop8(gone, a);
+    if (DROP && kBits) drop8(gone, a);
+    if (DROP && !kBits) drop8_at(d, u, a);
     if (ADD) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] = b[j] + a[j];

@@ -22,7 +22,7 @@ __device__ __forceinline__ uint32_t row_of(const Ids& ids, int64_t i) {
 
 // out[i, c] = id_i is a row and not dropped(i * dim + c) ? table[id_i, c] * c0 : 0.
 //
-// A row is vpr = ceil(dim / 8) vectors.  A lane takes up to kLookUnroll vectors at fixed
+// A row is vpr = ceil(dim / 8) vectors.  A lane takes up to look_unroll vectors at fixed
 // distances, whose loads are in flight together before the first store; the work per
 // vector has to stay near the 20 instructions of widening, scaling and rounding, or the
 // VALU and not the memory sets the pace (with each lane finding row and column of
@@ -34,12 +34,16 @@ __device__ __forceinline__ uint32_t row_of(const Ids& ids, int64_t i) {
 // blocks in order write memory in order.
 // Else a block holds `side` rows side by side, lane t being vector t mod vpr of row
 // t / vpr, `per` times; magic = floor(2^32 / vpr) + 1, so (t * magic) >> 32 == t / vpr.
-constexpr int kLookBlock = 256, kLookUnroll = 4;
+// With dropout a lane takes one vector: the generator's 1,000 cycles a vector leave the
+// memory time, and four generators' code does not fit the instruction cache.
+constexpr int kLookBlock = 256;
+constexpr int look_unroll(bool drop) { return drop ? 1 : 4; }
 struct LookShape { int64_t n, dim, tiles; uint64_t magic; int vpr, cols, width, wide_log2, side, per; };
 
 template <typename T, typename O, bool DROP, bool WIDE>
 __global__ __launch_bounds__(kLookBlock) void k_lookup(const T* __restrict__ table, Ids ids, LookShape s,
                                                        float c0, DropArgs da, O* __restrict__ out) {
+    constexpr int U = look_unroll(DROP);
     DropKey d{};
     if (DROP) d = drop_key(da);
     const int tid = threadIdx.x;
@@ -63,10 +67,10 @@ __global__ __launch_bounds__(kLookBlock) void k_lookup(const T* __restrict__ tab
             return 8 * (int64_t)(WIDE ? v + (u & ((1 << s.wide_log2) - 1)) * s.width : v);
         };
         const int vectors = WIDE ? s.per << s.wide_log2 : s.per;
-        Raw8<T> r[kLookUnroll];
-        bool in[kLookUnroll], is_row[kLookUnroll];
+        Raw8<T> r[U];
+        bool in[U], is_row[U];
 #pragma unroll
-        for (int u = 0; u < kLookUnroll; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int64_t row = row_at(u), col = col_at(u), left = s.dim - col;
             in[u] = is_row[u] = false;
             if (u >= vectors || row >= s.n) continue;
@@ -79,23 +83,27 @@ __global__ __launch_bounds__(kLookBlock) void k_lookup(const T* __restrict__ tab
                 r[u] = left >= 8 ? load8<false>(p) : load8_part(p, (int)left);
             }
         }
-        // The masks need no data: they are drawn while the loads are on their way, in
-        // a loop of their own that holds the generator's code once.
-        uint32_t gone = 0;
+        // The mask needs no data: it is drawn while the load is on its way.  Where a row is
+        // not a whole number of generator blocks it comes as bits from two of them.
+        uint32_t gone = 0, numbers[8];
+        const bool bits = (s.dim & 7) != 0;
         if (DROP) {
-#pragma unroll 1
-            for (int u = 0; u < vectors; ++u)
-                gone |= dropped8(d, (uint64_t)(row_at(u) * s.dim + col_at(u))) << 8 * u;
+            const uint64_t first = (uint64_t)(row_at(0) * s.dim + col_at(0));
+            if (bits) gone = dropped8(d, first);
+            else drop_numbers(d, first >> 3, numbers);
         }
 #pragma unroll
-        for (int u = 0; u < kLookUnroll; ++u) {
+        for (int u = 0; u < U; ++u) {
             if (!in[u]) continue;
             float a[8] = {};
             if (is_row[u]) {
                 widen(r[u], a);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) a[j] = a[j] * c0;
-                if (DROP) drop8(gone >> 8 * u, a);
+                if (DROP) {
+                    if (bits) drop8(gone, a);
+                    else drop8_at(d, numbers, a);
+                }
             }
             const int64_t col = col_at(u), left = s.dim - col;
             O* p = out + row_at(u) * s.dim + col;

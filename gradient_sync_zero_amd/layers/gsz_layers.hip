@@ -197,7 +197,7 @@ extern "C" int gsz_embedding_lookup(const void* table, int32_t table_type, int64
     l.vpr = (int)((dim + 7) / 8);
     const bool wide = l.vpr > kLookBlock / 2;
     // Vectors per lane: fewer where a few thousand blocks are all there is.
-    int vectors = kLookUnroll;
+    int vectors = look_unroll(da.threshold != 0);
     while (vectors > 1 && n * l.vpr / (kLookBlock * vectors) < 4096) vectors /= 2;
     l.side = wide ? 1 : kLookBlock / l.vpr;
     l.per = vectors;
@@ -283,8 +283,11 @@ extern "C" int gsz_embedding_grad(const void* ids, int32_t id_type, int64_t n, c
     const int join_tiles = (int)((dim + kJoinCols - 1) / kJoinCols);
     const int64_t join_blocks = (g.chunks + kJoinChunks - 1) / kJoinChunks * join_tiles;
     const int64_t rank_blocks = (n + kRankTokens - 1) / kRankTokens > clear_blocks ? (n + kRankTokens - 1) / kRankTokens : clear_blocks;
-    if (sum_blocks + (rank ? 0 : clear_blocks) + 256 > kMaxWorkItems / kGradBlock ||
-        join_blocks > kMaxWorkItems / kJoinBlock || (rank && rank_blocks > kMaxWorkItems / kRankBlock)) {
+    const SortShape sh = sort_shape(n, rows);                        // of the counting sort
+    const int parts = 2 * sh.passes - 1;                             // its launches that clear
+    if (sum_blocks + (direct ? clear_blocks : 0) > kMaxWorkItems / kGradBlock ||
+        join_blocks > kMaxWorkItems / kJoinBlock || (rank && rank_blocks > kMaxWorkItems / kRankBlock) ||
+        (!direct && !rank && sh.tiles + clear_blocks / parts + 1 > kMaxWorkItems / kSortBlock)) {
         set_error("%s: n %lld by dim %lld, or rows %lld, needs more than 2^31 work-items", who, (long long)n, (long long)dim, (long long)rows);
         return GSZ_ERR_SIZE;
     }
@@ -321,12 +324,10 @@ extern "C" int gsz_embedding_grad(const void* ids, int32_t id_type, int64_t n, c
         });
         if ((rc = launched(who))) return rc;
     } else {
-        const SortShape sh = sort_shape(n, rows);
         SortPass s{id, nullptr, nullptr, n, sh.rounds, sh.tiles, 0, 1 << sh.bits};
         uint32_t* count = u32(w.count);
         uint32_t* owner = accumulate ? nullptr : u32(w.owner);
         // The launches after the first each clear a part of the rows.
-        const int parts = 2 * sh.passes - 1;
         int part = 0;
         auto next_part = [&]() -> int64_t {                          // its blocks
             clear.first_block = accumulate ? 0xFFFFFFFFu : (unsigned)sh.tiles;
