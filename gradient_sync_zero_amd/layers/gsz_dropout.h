@@ -280,6 +280,12 @@ __device__ __forceinline__ uint32_t dropped_row(const DropKey& d, uint64_t first
 // y[e] = (add[e] or 0) + (dropped(e) ? 0 : x[e] * k), e in [0, n): one fp32
 // multiplication, one fp32 addition, one rounding to T.  A wave takes one tile, a lane
 // draws one generator block.
+//
+// Bound by memory, the generator's 20 products of 32 bits (v_mad_u64_u32) and 60 other
+// instructions for 8 elements just behind it: 512 Mi bf16 elements added to a stream of as
+// many in 490 us (6.57 TB/s; 2 GiB copied by torch: 4.9), 48 Mi fp32 from an odd place in 64 us
+// (6.3 TB/s; with each lane's 8 values in a row, half a line an access, 74).  One wave per
+// block; four took 507 us.  A whole 32-bit word per element would take twice the products.
 constexpr int kDropBlock = 64, kDropTile = kDropBlock / 64 * kTile;
 template <typename T, bool ADD, bool DROP, bool FULL>
 __device__ __forceinline__ void dropout_tile(const T* x, const T* add, T* y, int64_t e, int64_t left,

@@ -34,8 +34,16 @@ __device__ __forceinline__ uint32_t row_of(const Ids& ids, int64_t i) {
 // blocks in order write memory in order.
 // Else a block holds `side` rows side by side, lane t being vector t mod vpr of row
 // t / vpr, `per` times; magic = floor(2^32 / vpr) + 1, so (t * magic) >> 32 == t / vpr.
-// With dropout a lane takes one vector: the generator's 1,000 cycles a vector leave the
+// With dropout a lane takes one vector: the generator's 700 cycles a vector leave the
 // memory time, and four generators' code does not fit the instruction cache.
+//
+// Bound by memory: 64 Ki tokens of 8192 bf16 columns (1.07 GB out, 14,000 distinct rows) in
+// 246 us; counters show 1.07 GB written and 0.73 GB fetched, 7.3 TB/s, since the L2s do
+// not hold the rows until they come again.  Two ways to have them do so fetched 0.45 GB
+// and lost: eight column slices, one for each XCD (281 us: rows in pieces of 2 KB; 13%
+// faster where the table's rows lie in the memory-side cache), and each row on the XCD of
+// its number (296 us: fewer loads in flight).  8192 tokens of 768 columns with dropout,
+// 18 MB: 8.2 us, the generator and the latency of id, row and store.
 constexpr int kLookBlock = 256;
 constexpr int look_unroll(bool drop) { return drop ? 1 : 4; }
 struct LookShape { int64_t n, dim, tiles; uint64_t magic; int vpr, cols, width, wide_log2, side, per; };
@@ -117,7 +125,9 @@ __global__ __launch_bounds__(kLookBlock) void k_lookup(const T* __restrict__ tab
 //
 // With accumulate = 0 the rows without a token are cleared.  No launch does only
 // that: the blocks that clear ride along with the sort, whose few blocks leave
-// the memory idle.
+// the memory idle.  292 MB in three launches of 17.7 us (5.5 TB/s, the sort's own 4-5 us
+// a launch hidden).  Clearing part of it beside the sums instead was 2.5% slower on that
+// gradient, 6% faster on one of 508 MB and few tokens.
 
 // Clears the rows r0 + i, i a set bit of `missing`, with `threads` threads: neighbours
 // as one stretch of memory in whole 16-byte vectors, whatever the rows' alignment (row by
@@ -261,7 +271,9 @@ __global__ __launch_bounds__(kRankBlock) void k_rank(Ids ids, int n, uint32_t* _
 
 // More tokens: stable counting passes over digits of the key, lowest first, a launch
 // to count and one to place each.  count[tile][digit]: how often a digit occurs in a
-// tile of `rounds` times kSortTile tokens.  (Counting the next digit while placing this
+// tile of `rounds` times kSortTile tokens.  64 Ki tokens in four launches of 3.4 to 5 us,
+// all latency; tiles of 512 tokens, one per work-item, beat 1024 of four (16 Ki tokens 3 us
+// slower, for want of blocks) and 256 (more counts to add up).  (Counting the next digit while placing this
 // one, with an atomic per token where it lands, saved a launch and cost 10 us of
 // atomics on 16 Ki tokens.)
 constexpr int kSortWaves = kSortBlock / 64, kSortMaxBins = 1024;
@@ -415,9 +427,16 @@ __global__ __launch_bounds__(kSortBlock) void k_place(SortPass s, const uint32_t
 // The sorted tokens are cut into chunks of K; one wave sums the runs of equal rows
 // of one chunk over one tile of columns, in fp32, positions rising.  A run that
 // starts in a chunk and ends at most K tokens past it is finished by that chunk's
-// wave (the next chunk's skips it).  A longer run leaves an fp32 partial sum per chunk,
+// wave (the next chunk's skips it): without that, most chunks of a Zipf-like text would
+// end inside a run and write and read two fp32 rows more.  A longer run leaves an fp32 partial sum per chunk,
 // part[2c + 1] where it starts in chunk c and part[2c] where it came from an earlier
 // one; k_join adds them in chunk order.
+//
+// Bound by memory, rows of dy read in the tokens' order and not their own: 64 Ki tokens of
+// 8192 bf16 columns, 1.07 GB read and 0.26 GB written, in 253 us (5.3 TB/s; a gather that
+// only reads reaches as much); 16 Ki tokens of 2048 added into fp32 in 35 us (0.18 GB by
+// the counters, 5.0 TB/s).  One wave per block and four rows in flight beat four waves by
+// 2-5% and eight rows by 0-4%.
 
 constexpr int kGradBlock = 64, kGradWaves = kGradBlock / 64, kGradCols = kTile, kGradUnroll = 4;
 constexpr int kMaxChunk = 32;                         // a wave holds 2 K keys
@@ -529,7 +548,9 @@ __global__ __launch_bounds__(kGradBlock) void k_grad(const T* __restrict__ dy, c
 // Finishes the runs that k_grad left in parts.  A block looks at kJoinChunks chunks and takes
 // kJoinCols columns of the runs that start in one of them and leave a tail part: a run
 // of at most kJoinWaves parts is one wave's, a longer one the block's, each wave
-// summing a stretch of its parts and the first wave those sums, all in order.
+// summing a stretch of its parts and the first wave those sums, all in order.  5.5 to 14 us,
+// the latency of keys, parts and row; blocks of 1024 over 64 chunks took 19 where these
+// take 14.
 constexpr int kJoinBlock = 512, kJoinWaves = kJoinBlock / 64, kJoinCols = 256, kJoinChunks = 32;
 // a + part rows [k, end) of the run that starts in `chunk`, at the lane's columns.
 __device__ __forceinline__ f32x4 sum_parts(const float* __restrict__ part, int64_t pitch, int64_t chunk,
@@ -616,7 +637,8 @@ __global__ __launch_bounds__(kJoinBlock) void k_join(const uint32_t* __restrict_
 
 // ---------------------------------------------------- a few tokens at once --
 
-// n <= kDirectMax tokens in one launch without a sort: the wave of (token, tile of
+// n <= kDirectMax tokens in one launch without a sort (64 tokens of 8192 columns added into
+// fp32 in 3.8 us; sort, sums and join are three launches, 8.5 us a call at 130 tokens): the wave of (token, tile of
 // columns) ends if its row came earlier, else it sums the tokens of its row in order.
 // Blocks from clear.first_block on clear the rows that no token has.
 constexpr int kDirectMax = 128, kDirectUnroll = 8;
