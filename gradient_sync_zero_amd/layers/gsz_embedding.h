@@ -273,9 +273,9 @@ __global__ __launch_bounds__(kRankBlock) void k_rank(Ids ids, int n, uint32_t* _
 // to count and one to place each.  count[tile][digit]: how often a digit occurs in a
 // tile of `rounds` times kSortTile tokens.  64 Ki tokens in four launches of 3.4 to 5 us,
 // all latency; tiles of 512 tokens, one per work-item, beat 1024 of four (16 Ki tokens 3 us
-// slower, for want of blocks) and 256 (more counts to add up).  (Counting the next digit while placing this
-// one, with an atomic per token where it lands, saved a launch and cost 10 us of
-// atomics on 16 Ki tokens.)
+// slower, for want of blocks) and 256 (more counts to add up).  Counting the next digit
+// while placing this one, with an atomic per token where it lands, saved a launch and cost
+// 10 us of atomics on 16 Ki tokens.
 constexpr int kSortWaves = kSortBlock / 64, kSortMaxBins = 1024;
 constexpr int kSortPer = 1, kSortTile = kSortBlock * kSortPer;
 constexpr int kSortBinsPer = kSortMaxBins / kSortBlock;
@@ -428,9 +428,9 @@ __global__ __launch_bounds__(kSortBlock) void k_place(SortPass s, const uint32_t
 // of one chunk over one tile of columns, in fp32, positions rising.  A run that
 // starts in a chunk and ends at most K tokens past it is finished by that chunk's
 // wave (the next chunk's skips it): without that, most chunks of a Zipf-like text would
-// end inside a run and write and read two fp32 rows more.  A longer run leaves an fp32 partial sum per chunk,
-// part[2c + 1] where it starts in chunk c and part[2c] where it came from an earlier
-// one; k_join adds them in chunk order.
+// end inside a run and write and read two fp32 rows more.  A longer run leaves an fp32
+// partial sum per chunk, part[2c + 1] where it starts in chunk c and part[2c] where it
+// came from an earlier one; k_join adds them in chunk order.
 //
 // Bound by memory, rows of dy read in the tokens' order and not their own: 64 Ki tokens of
 // 8192 bf16 columns, 1.07 GB read and 0.26 GB written, in 253 us (5.3 TB/s; a gather that

@@ -266,6 +266,39 @@ def test_grad_many_tokens(n, kind):
     check_grad(n, 5000, 24, kind, BF, F32, acc=n % 2 == 0)
 
 
+@pytest.mark.parametrize("n", [1, 5, 64, 128, 129, 700, 9000])
+@pytest.mark.parametrize("dim", [40, 41, 520])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_grad_with_dropout_on_every_path(n, dim, dt):
+    check_grad(n, 60, dim, "any", dt, F32, acc=n % 2 == 0, p=0.3, scale=0.5, shift=n % 3)
+    check_grad(n, 60, dim, "one", dt, BF, acc=n % 2 == 1, p=0.7)
+
+
+@pytest.mark.parametrize("dt,gt", [(BF, BF), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("dim,kind", [(2048, "any"), (2051, "hot")])
+@pytest.mark.parametrize("acc", [False, True])
+def test_grad_of_large_dy(dt, gt, dim, kind, acc):
+    """dy of over 64 MiB, which is read nontemporally, against torch in 64 bits."""
+    n, rows = 18_000, 3000
+    rng = np.random.default_rng(dim)
+    ids = torch.from_numpy(make_ids(kind, n, rows, rng)).cuda()
+    gen = torch.Generator(device="cuda").manual_seed(dim)
+    dy = torch.randn(n, dim, device="cuda", generator=gen).to(dt)
+    old = torch.randn(rows, dim, device="cuda", generator=gen).to(gt)
+    grad = old.clone() if acc else torch.full_like(old, float("nan"))
+    run_grad(ids, dy, grad, scale=3.0, accumulate=acc)
+    ok = (ids >= 0) & (ids < rows)
+    ref = torch.zeros(rows, dim, dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(ref)
+    ref.index_add_(0, ids[ok], dy[ok].double())
+    size.index_add_(0, ids[ok], dy[ok].double().abs())
+    ref, size = ref * 3 + (old.double() if acc else 0), size * 3
+    m = torch.bincount(ids[ok], minlength=rows).double()[:, None]
+    # torch's own 64-bit sums are off by at most m 2^-53 of size: far below EPS size
+    bound = size * ((1 + EPS) ** (m + 4) - 1) * (1 + U[gt]) * (1 + EPS) + ref.abs() * ((1 + EPS) * (1 + U[gt]) - 1) + TINY[gt]
+    assert bool(((grad.double() - ref).abs() <= bound).all())
+
+
 @pytest.mark.parametrize("rows", [0, 1, 2, 255, 256, 1023, 1024, 70_000, (1 << 20) - 1, 1 << 20, 1_100_003])
 def test_grad_table_heights(rows):
     """One to three passes of the counting sort, keys at the digits' borders."""
@@ -354,6 +387,27 @@ def test_on_another_stream():
         outs.append((out, y, grad))
     for o in outs[1:]:
         assert all(torch.equal(a, b) for a, b in zip(o, outs[0]))
+
+
+def test_two_calls_at_once():
+    """Two gradients on two streams with a workspace each, over and over, have the
+    bits that each has alone."""
+    rng = np.random.default_rng(31)
+    rows, dim = 4000, 512
+    cases = []
+    for n in (9000, 3000):
+        ids, dy = torch.from_numpy(make_ids("hot", n, rows, rng)).cuda(), draw(rng, (n, dim), BF)
+        alone = torch.empty(rows, dim, device="cuda")
+        run_grad(ids, dy, alone)
+        ws = torch.empty(G.embedding_workspace_bytes(n, rows, dim), dtype=torch.uint8, device="cuda")
+        cases.append((ids, dy, ws, alone, torch.cuda.Stream(), [torch.empty_like(alone) for _ in range(5)]))
+    torch.cuda.synchronize()
+    for k in range(5):
+        for ids, dy, ws, _, st, outs in cases:
+            G.embedding_grad(ids, dy, outs[k], ws, stream=st)
+    torch.cuda.synchronize()
+    for *_, alone, _, outs in cases:
+        assert all(torch.equal(o, alone) for o in outs)
 
 
 @pytest.mark.parametrize("n", [300, 9000])
