@@ -42,7 +42,8 @@ __device__ __forceinline__ uint32_t row_of(const Ids& ids, int64_t i) {
 // not hold the rows until they come again.  Two ways to have them do so fetched 0.45 GB
 // and lost: eight column slices, one for each XCD (281 us: rows in pieces of 2 KB; 13%
 // faster where the table's rows lie in the memory-side cache), and each row on the XCD of
-// its number (296 us: fewer loads in flight).  8192 tokens of 768 columns with dropout,
+// its number (266 us with a token to a block, 296 with several: every block first votes on
+// the ids of 64 tokens).  8192 tokens of 768 columns with dropout,
 // 18 MB: 8.2 us, the generator and the latency of id, row and store.
 constexpr int kLookBlock = 256;
 constexpr int look_unroll(bool drop) { return drop ? 1 : 4; }
