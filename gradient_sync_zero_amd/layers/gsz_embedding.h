@@ -639,9 +639,9 @@ __global__ __launch_bounds__(kJoinBlock) void k_join(const uint32_t* __restrict_
 // ---------------------------------------------------- a few tokens at once --
 
 // n <= kDirectMax tokens in one launch without a sort (64 tokens of 8192 columns added into
-// fp32 in 3.8 us; sort, sums and join are three launches, 8.5 us a call at 130 tokens):
-// the wave of (token, tile of columns) ends if its row came earlier, else it sums the
-// tokens of its row in order.
+// fp32 in 3.8 us; a call of 128 tokens of 4096 columns 6.9 us against 13.2 by sort, sums
+// and join, and 17 against 13 where nine in ten are one row's): the wave of (token, tile
+// of columns) ends if its row came earlier, else it sums the tokens of its row in order.
 // Blocks from clear.first_block on clear the rows that no token has.
 constexpr int kDirectMax = 128, kDirectUnroll = 8;
 template <typename T, typename G, bool ACC, bool DROP>
