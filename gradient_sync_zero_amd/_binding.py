@@ -670,7 +670,8 @@ def embedding_lookup(ids, table, out, scale=1.0, p=0.0, rng=None, site=0, stream
 
 
 def embedding_workspace_bytes(n, rows, dim):
-    """Device scratch bytes for embedding_grad of n tokens on a (rows, dim) table."""
+    """Device scratch bytes for embedding_grad of n tokens, or fewer, on a (rows, dim)
+    table."""
     out = ctypes.c_size_t()
     _check(load().gsz_embedding_workspace_bytes(int(n), int(rows), int(dim), ctypes.byref(out)))
     return out.value

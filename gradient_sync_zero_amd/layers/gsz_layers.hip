@@ -90,13 +90,14 @@ int grid_for(int64_t tiles, int block) {
 
 // ------------------------------------------------------- gradient's plan --
 
-// The counting sort of n > kRankMax tokens: at most 256 tiles (every block of a pass
+// The counting sort of n > kRankMax tokens: at most kMaxTiles tiles (every block of a pass
 // reads the digit counts of all of them) and digits of at most 10 bits.
+constexpr int kMaxTiles = 256;
 struct SortShape { int64_t rounds; int tiles, bits, passes; };
 SortShape sort_shape(int64_t n, int64_t rows) {
     SortShape s{};
     s.rounds = 1;
-    while ((n + s.rounds * kSortTile - 1) / (s.rounds * kSortTile) > 256) s.rounds *= 2;
+    while ((n + s.rounds * kSortTile - 1) / (s.rounds * kSortTile) > kMaxTiles) s.rounds *= 2;
     s.tiles = (int)((n + s.rounds * kSortTile - 1) / (s.rounds * kSortTile));
     int bits = 1;
     while (((int64_t)1 << bits) <= rows) ++bits;          // keys [0, rows]
@@ -111,12 +112,24 @@ int col_tiles(int64_t dim) { return (int)((dim + kGradCols - 1) / kGradCols); }
 // tokens of 768 columns 39.0 us against 36.5.  8192 waves: 4096 tokens of 4096 columns
 // 26.9 us against 25.7, one row with nine tokens in ten 198 us against 193; 2048 waves:
 // 8192 tokens of 4096 columns 49.5 us against 48.1.)
+constexpr int kGradMinWaves = 4096, kMinChunk = 4;
 int chunk_for(int64_t n, int64_t dim) {
     int K = kMaxChunk;
-    while (K > 4 && (n + K - 1) / K * col_tiles(dim) < 4096) K /= 2;
+    while (K > kMinChunk && (n + K - 1) / K * col_tiles(dim) < kGradMinWaves) K /= 2;
     return K;
 }
+// The most chunks that n tokens or fewer are cut into.  K falls as n does, so a few tokens
+// less can be up to twice as many chunks.  With c = ceil(kGradMinWaves / column tiles), n is
+// cut by less than kMaxChunk only where ceil(n / 2 K) < c, into ceil(n / K) <= 2 (c - 1) chunks.
+int64_t most_chunks(int64_t n, int64_t dim) {
+    const int64_t c = dim > 0 ? (kGradMinWaves + col_tiles(dim) - 1) / col_tiles(dim) : 1;
+    const int64_t fine = (n + kMinChunk - 1) / kMinChunk, coarse = (n + kMaxChunk - 1) / kMaxChunk;
+    const int64_t most = fine < 2 * (c - 1) ? fine : 2 * (c - 1);
+    return coarse > most ? coarse : most;
+}
 
+// A workspace for n tokens serves every smaller call on the same table: no part of it
+// shrinks as n grows.
 struct Workspace { size_t key[2], pos[2], count, owner, part, bytes; };
 Workspace workspace_for(int64_t n, int64_t rows, int64_t dim) {
     Workspace w{};
@@ -126,12 +139,11 @@ Workspace workspace_for(int64_t n, int64_t rows, int64_t dim) {
     const bool rank = n <= kRankMax;
     for (int k = 0; k < (rank ? 1 : 2); ++k) { w.key[k] = take(4 * n); w.pos[k] = take(4 * n); }
     if (!rank) {
-        const SortShape s = sort_shape(n, rows);
-        w.count = take((size_t)4 * s.tiles << s.bits);
+        const int64_t tiles = (n + kSortTile - 1) / kSortTile;
+        w.count = take((size_t)4 * (tiles < kMaxTiles ? tiles : kMaxTiles) << sort_shape(n, rows).bits);
         w.owner = take((size_t)4 * rows);
     }
-    const int64_t chunks = (n + chunk_for(n, dim) - 1) / chunk_for(n, dim);
-    w.part = take((size_t)8 * chunks * ((dim + 7) / 8 * 8));
+    w.part = take((size_t)8 * most_chunks(n, dim) * ((dim + 7) / 8 * 8));
     w.bytes = at;
     return w;
 }

@@ -429,8 +429,9 @@ int gsz_embedding_lookup(const void* table, int32_t table_type, int64_t rows, in
 /* *out = bytes of device scratch gsz_embedding_grad needs for these sizes, per call
  * in flight (two captured graphs that may run at once need one each): none for n <= 128,
  * else the sorted tokens, fp32 partial sums of rows with many tokens (2 * n * dim bytes
- * for small n, an eighth of that for large n) and, for n > 8192, 4 bytes a row.  Needs no
- * initialisation.  Errors as gsz_embedding_lookup's sizes. */
+ * for small n, an eighth of that for large n) and, for n > 8192, 4 bytes a row.  Never
+ * less for a larger n: on one table, the bytes for the largest batch serve every smaller one.
+ * Needs no initialisation.  Errors as gsz_embedding_lookup's sizes. */
 int gsz_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim, size_t* out);
 
 /* Gradient of gsz_embedding_lookup with respect to the table:
