@@ -157,8 +157,9 @@ __device__ __forceinline__ void clear_rows(G* __restrict__ grad, int64_t dim, in
 
 constexpr int kSortBlock = 512;                       // of the launches that clear beside the sort
 
-// Which part of the table a launch clears: `per` rows (at most 64) for each of its
-// blocks from `first_block` on, rows [row0, row1).
+// Which part of the table a launch clears: rows [row0, row1), `per` (at most 64) at a time
+// for each of its blocks from `first_block` on.  There is a block for every `per` rows, as
+// long as the launch can hold so many; tables of over 10^9 narrow rows take several turns.
 struct ClearShape { void* grad; int64_t dim, row0, row1; unsigned first_block; int per, f32; };
 
 // owner[v] is some token of row v, if there is one: k_count stores every token's
@@ -166,17 +167,19 @@ struct ClearShape { void* grad; int64_t dim, row0, row1; unsigned first_block; i
 // is never cleared: what it holds counts only if that token does have row v.
 __device__ __forceinline__ void clear_block(const ClearShape& c, const Ids& ids, int64_t n,
                                             const uint32_t* __restrict__ owner) {
-    const int64_t r0 = c.row0 + (int64_t)(blockIdx.x - c.first_block) * c.per;
-    const int lane = threadIdx.x & 63;
-    const int64_t v = r0 + lane;
-    bool missing = lane < c.per && v < c.row1;
-    if (missing) {
-        const uint32_t i = owner[v];
-        missing = !(i < (uint64_t)n && row_of(ids, i) == (uint32_t)v);
+    const int64_t turn = (int64_t)(gridDim.x - c.first_block) * c.per;
+    for (int64_t r0 = c.row0 + (int64_t)(blockIdx.x - c.first_block) * c.per; r0 < c.row1; r0 += turn) {
+        const int lane = threadIdx.x & 63;
+        const int64_t v = r0 + lane;
+        bool missing = lane < c.per && v < c.row1;
+        if (missing) {
+            const uint32_t i = owner[v];
+            missing = !(i < (uint64_t)n && row_of(ids, i) == (uint32_t)v);
+        }
+        const uint64_t m = __ballot(missing);
+        if (c.f32) clear_rows(static_cast<float*>(c.grad), c.dim, r0, m, threadIdx.x, kSortBlock);
+        else clear_rows(static_cast<uint16_t*>(c.grad), c.dim, r0, m, threadIdx.x, kSortBlock);
     }
-    const uint64_t m = __ballot(missing);
-    if (c.f32) clear_rows(static_cast<float*>(c.grad), c.dim, r0, m, threadIdx.x, kSortBlock);
-    else clear_rows(static_cast<uint16_t*>(c.grad), c.dim, r0, m, threadIdx.x, kSortBlock);
 }
 
 // ------------------------------------------------------------------ sort --
@@ -650,13 +653,16 @@ __global__ __launch_bounds__(kGradBlock) void k_direct(const T* __restrict__ dy,
     const int lane = threadIdx.x & 63;
     const uint32_t k0 = lane < s.n ? row_of(ids, lane) : s.rows, k1 = lane + 64 < s.n ? row_of(ids, lane + 64) : s.rows;
     if (!ACC && blockIdx.x >= clear.first_block) {
-        const int64_t r0 = (int64_t)(blockIdx.x - clear.first_block) * clear.per, v = r0 + lane;
-        bool missing = lane < clear.per && v < clear.row1;
-        for (int j = 0; j < 64; ++j) {
-            if ((uint32_t)__builtin_amdgcn_readlane(k0, j) == (uint64_t)v) missing = false;
-            if ((uint32_t)__builtin_amdgcn_readlane(k1, j) == (uint64_t)v) missing = false;
+        const int64_t turn = (int64_t)(gridDim.x - clear.first_block) * clear.per;
+        for (int64_t r0 = (int64_t)(blockIdx.x - clear.first_block) * clear.per; r0 < clear.row1; r0 += turn) {
+            const int64_t v = r0 + lane;
+            bool missing = lane < clear.per && v < clear.row1;
+            for (int j = 0; j < 64; ++j) {
+                if ((uint32_t)__builtin_amdgcn_readlane(k0, j) == (uint64_t)v) missing = false;
+                if ((uint32_t)__builtin_amdgcn_readlane(k1, j) == (uint64_t)v) missing = false;
+            }
+            clear_rows(grad, s.dim, r0, __ballot(missing), threadIdx.x, kGradBlock);
         }
-        clear_rows(grad, s.dim, r0, __ballot(missing), threadIdx.x, kGradBlock);
         return;
     }
     const int64_t w = (int64_t)blockIdx.x * kGradWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

@@ -299,17 +299,22 @@ extern "C" int gsz_embedding_grad(const void* ids, int32_t id_type, int64_t n, c
     auto clamp = [](int64_t v, int64_t most) { return (int)(v < 1 ? 1 : v > most ? most : v); };
     int per = rank ? clamp(((int64_t)256 << 10) / (64 * row_bytes), 64) : clamp(((int64_t)32 << 10) / row_bytes, 64);
     while (rank && per & (per - 1)) per &= per - 1;                  // a power of two
-    const int64_t clear_blocks = accumulate ? 0 : (rows + (int64_t)per * (rank ? 64 : 1) - 1) / ((int64_t)per * (rank ? 64 : 1));
+    const int64_t rank_max = kMaxWorkItems / kRankBlock, direct_max = kMaxWorkItems / kGradBlock;
+    auto clear_for = [&] { return accumulate ? 0 : (rows + (int64_t)per * (rank ? 64 : 1) - 1) / ((int64_t)per * (rank ? 64 : 1)); };
+    while (rank && per < 64 && clear_for() > rank_max) per *= 2;
+    int64_t clear_blocks = clear_for();                              // the other sort divides them over its launches
     const int64_t sum_blocks = ((direct ? n : g.chunks) * g.tiles + kGradWaves - 1) / kGradWaves;
+    if (direct && clear_blocks > 0 && clear_blocks > direct_max - sum_blocks)
+        clear_blocks = direct_max > sum_blocks ? direct_max - sum_blocks : 1;
     const int join_tiles = (int)((dim + kJoinCols - 1) / kJoinCols);
     const int64_t join_blocks = (g.chunks + kJoinChunks - 1) / kJoinChunks * join_tiles;
     const int64_t rank_blocks = (n + kRankTokens - 1) / kRankTokens > clear_blocks ? (n + kRankTokens - 1) / kRankTokens : clear_blocks;
     const SortShape sh = sort_shape(n, rows);                        // of the counting sort
     const int parts = 2 * sh.passes - 1;                             // its launches that clear
-    if (sum_blocks + (direct ? clear_blocks : 0) > kMaxWorkItems / kGradBlock ||
-        join_blocks > kMaxWorkItems / kJoinBlock || (rank && rank_blocks > kMaxWorkItems / kRankBlock) ||
-        (!direct && !rank && sh.tiles + clear_blocks / parts + 1 > kMaxWorkItems / kSortBlock)) {
-        set_error("%s: n %lld by dim %lld, or rows %lld, needs more than 2^31 work-items", who, (long long)n, (long long)dim, (long long)rows);
+    const int64_t sort_max = kMaxWorkItems / kSortBlock - sh.tiles;  // blocks that each of them has for it
+    if (sum_blocks + (direct ? clear_blocks : 0) > direct_max || (!direct && join_blocks > kMaxWorkItems / kJoinBlock) ||
+        (rank && rank_blocks > rank_max) || (!direct && !rank && sort_max < 1)) {
+        set_error("%s: n %lld by dim %lld needs more than 2^31 work-items", who, (long long)n, (long long)dim);
         return GSZ_ERR_SIZE;
     }
     if ((rc = check_device(who))) return rc;
@@ -354,7 +359,8 @@ extern "C" int gsz_embedding_grad(const void* ids, int32_t id_type, int64_t n, c
             clear.first_block = accumulate ? 0xFFFFFFFFu : (unsigned)sh.tiles;
             clear.row0 = clear_blocks * part / parts * per;
             clear.row1 = ++part == parts ? rows : clear_blocks * part / parts * per;
-            return accumulate ? 0 : (clear.row1 - clear.row0 + per - 1) / per;
+            const int64_t blocks = accumulate ? 0 : (clear.row1 - clear.row0 + per - 1) / per;
+            return blocks < sort_max ? blocks : sort_max;
         };
         for (int k = 0; k < sh.passes; ++k) {
             s.shift = k * sh.bits;

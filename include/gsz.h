@@ -449,7 +449,9 @@ int gsz_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim, size_t* 
  *   ws (device, 16-byte aligned, >= gsz_embedding_workspace_bytes): scratch (GSZ_ERR_SIZE
  *     if too small); may be NULL where none is needed.
  * Errors as gsz_embedding_lookup; GSZ_ERR_SIZE too if a launch would need more than
- * 2^31 work-items (n * dim over about 2^39, or n over 2^29). */
+ * 2^31 work-items: with t = ceil(dim / 512), n * t over 2^25 for n <= 128 (2^25 - 1 with
+ * accumulate = 0), ceil(n / 32) * t over 2^25 for more tokens (n over 2^30 up to 512
+ * columns). */
 int gsz_embedding_grad(const void* ids, int32_t id_type, int64_t n, const void* dy, int32_t dy_type,
                        int64_t rows, int64_t dim, double scale, double p, const uint64_t* rng,
                        uint32_t site, void* grad, int32_t grad_type, int32_t accumulate, void* ws,
