@@ -54,6 +54,14 @@ int bad_arg(const char* who, const char* what) {
     return GSZ_ERR_INVALID_ARG;
 }
 
+// Whether a buffer that a call writes and one that it reads (or writes besides) share a byte.
+struct Span { const void* p; int64_t bytes; };
+bool overlap(Span a, Span b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && (x < y ? y - x < (uintptr_t)a.bytes : x - y < (uintptr_t)b.bytes);
+}
+Span rng_span(const DropArgs& d) { return {d.threshold ? d.rng : nullptr, 16}; }
+
 // The mask's arguments and the constant scale / (1 - threshold 2^-32), formed in
 // double and rounded once.
 int check_drop(const char* who, double p, double scale, const uint64_t* rng, uint32_t site,
@@ -174,6 +182,9 @@ extern "C" int gsz_dropout(const void* x, const void* add, void* y, int64_t n, i
     if (rc) return rc;
     if (n > 0 && (!x || !y)) return bad_arg(who, "NULL buffer");
     if (off_by(x, size) || off_by(y, size) || off_by(add, size)) { set_error("%s: a buffer is not aligned to its values", who); return GSZ_ERR_MISALIGNED; }
+    const Span out{y, n * size};
+    if ((y != x && overlap(out, {x, n * size})) || (y != add && overlap(out, {add, n * size})) || overlap(out, rng_span(da)))
+        return bad_arg(who, "y overlaps x, add or rng");
     if ((rc = check_device(who))) return rc;
     if (n == 0) return GSZ_OK;
     const int grid = grid_for((n + kDropTile - 1) / kDropTile, kDropBlock);
@@ -205,6 +216,9 @@ extern "C" int gsz_embedding_lookup(const void* table, int32_t table_type, int64
     const bool work = n > 0 && dim > 0;
     if (work && (!ids || !out || (rows > 0 && !table))) return bad_arg(who, "NULL buffer");
     if (off_by(table, ts) || off_by(out, os) || off_by(ids, is)) { set_error("%s: a buffer is not aligned to its values", who); return GSZ_ERR_MISALIGNED; }
+    const Span written{out, n * dim * os};
+    if (overlap(written, {table, rows * dim * ts}) || overlap(written, {ids, n * is}) || overlap(written, rng_span(da)))
+        return bad_arg(who, "out overlaps table, ids or rng");
     if ((rc = check_device(who))) return rc;
     if (!work) return GSZ_OK;
     LookShape l{};
@@ -317,6 +331,10 @@ extern "C" int gsz_embedding_grad(const void* ids, int32_t id_type, int64_t n, c
         set_error("%s: n %lld by dim %lld needs more than 2^31 work-items", who, (long long)n, (long long)dim);
         return GSZ_ERR_SIZE;
     }
+    const Span written{grad, rows * dim * gs}, scratch{ws, (int64_t)w.bytes}, read[] = {{ids, n * is}, {dy, n * dim * ds}, rng_span(da)};
+    for (const Span& r : read)
+        if (overlap(written, r) || overlap(scratch, r)) return bad_arg(who, "grad or ws overlaps ids, dy or rng");
+    if (overlap(written, scratch)) return bad_arg(who, "ws overlaps grad");
     if ((rc = check_device(who))) return rc;
 
     char* base = static_cast<char*>(ws);

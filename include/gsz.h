@@ -397,7 +397,7 @@ int gsz_adamw_step(float* master, float* m, float* v, const float* g, int64_t n,
  * is 0 whatever x holds (infinities and NaN too).
  *   x, y, add (device, n values of `type`: GSZ_TYPE_BF16 or GSZ_TYPE_F32; any
  *     address that is a multiple of the value's size); add may be NULL.  y may be
- *     x or add themselves; it must not overlap them otherwise.
+ *     x or add themselves; it must not overlap them otherwise (GSZ_ERR_INVALID_ARG).
  *   p: in [0, 1) (GSZ_ERR_INVALID_ARG otherwise).
  *   rng (device, two uint64: {seed, step}, 8-byte aligned; step is taken mod 2^32):
  *     read by the kernel, so a captured graph draws a new mask at each replay once
@@ -420,7 +420,7 @@ int gsz_dropout(const void* x, const void* add, void* y, int64_t n, int32_t type
  *   ids (device, n of GSZ_TYPE_I32 or GSZ_TYPE_I64); out (device, n * dim of out_type,
  *     any multiple of the value's size; must not overlap table or ids).
  * GSZ_ERR_SIZE if rows or n is over 2^31 - 1 or dim over 2^29;
- * GSZ_ERR_INVALID_ARG if p is not in [0, 1) or c0 is not finite in fp32. */
+ * GSZ_ERR_INVALID_ARG if p is not in [0, 1), c0 is not finite in fp32 or buffers overlap. */
 int gsz_embedding_lookup(const void* table, int32_t table_type, int64_t rows, int64_t dim,
                          const void* ids, int32_t id_type, int64_t n, double scale, double p,
                          const uint64_t* rng, uint32_t site, void* out, int32_t out_type,
@@ -447,7 +447,7 @@ int gsz_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim, size_t* 
  *     multiple of the value's size, so grad may be a tensor's place in a bf16 or fp32
  *     bucket-flat buffer.  It must not overlap dy or ids.
  *   ws (device, 16-byte aligned, >= gsz_embedding_workspace_bytes): scratch (GSZ_ERR_SIZE
- *     if too small); may be NULL where none is needed.
+ *     if too small), apart from the other buffers; may be NULL where none is needed.
  * Errors as gsz_embedding_lookup; GSZ_ERR_SIZE too if a launch would need more than
  * 2^31 work-items: with t = ceil(dim / 512), n * t over 2^25 for n <= 128 (2^25 - 1 with
  * accumulate = 0), ceil(n / 32) * t over 2^25 for more tokens (n over 2^30 up to 512

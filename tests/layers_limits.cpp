@@ -28,7 +28,8 @@ static void launch_checked(unsigned grid, unsigned block, std::function<void()> 
 
 static int sizes() {
     g_run = false;
-    void* const p = reinterpret_cast<void*>((uintptr_t)1 << 20);        // no launch runs: never read
+    auto at = [](int bit) { return reinterpret_cast<void*>((uintptr_t)1 << bit); };      // no launch runs: never read
+    void* const p = at(20);
     const int64_t K = 1 << 10, M = K * K, G = K * M, kRows = 2 * G - 1;
     struct Case { int64_t n, rows, dim; int acc, type, want; };
     const Case cases[] = {
@@ -50,18 +51,32 @@ static int sizes() {
     };
     int bad = 0;
     for (const Case& c : cases) {
-        const int rc = gsz_embedding_grad(p, GSZ_TYPE_I32, c.n, p, GSZ_TYPE_BF16, c.rows, c.dim, 1.0, 0.0, nullptr, 0, p, c.type,
-                                          c.acc, p, ~(size_t)0 >> 1, nullptr);
+        const int rc = gsz_embedding_grad(p, GSZ_TYPE_I32, c.n, at(44), GSZ_TYPE_BF16, c.rows, c.dim, 1.0, 0.0, nullptr, 0, at(61), c.type,
+                                          c.acc, at(62), ~(size_t)0 >> 1, nullptr);
         if (rc != c.want && ++bad)
             std::printf("gradient of %ld tokens, %ld rows of %ld, accumulate %d: %d, want %d\n", (long)c.n, (long)c.rows, (long)c.dim, c.acc, rc, c.want);
     }
     const int64_t lookups[][3] = {{kRows, kRows, 512 * M}, {kRows, kRows, 1}, {1, 1, 512 * M}, {kRows, 1, 8192}, {kRows, 1, 1023}};
     for (auto& l : lookups)
         for (double drop : {0.0, 0.5})
-            if (gsz_embedding_lookup(p, GSZ_TYPE_BF16, l[1], l[2], p, GSZ_TYPE_I64, l[0], 1.0, drop, (uint64_t*)p, 0, p, GSZ_TYPE_F32, nullptr) != GSZ_OK && ++bad)
+            if (gsz_embedding_lookup(at(61), GSZ_TYPE_BF16, l[1], l[2], at(40), GSZ_TYPE_I64, l[0], 1.0, drop, (uint64_t*)p, 0, at(62), GSZ_TYPE_F32, nullptr) != GSZ_OK && ++bad)
                 std::printf("lookup of %ld tokens of %ld columns refused\n", (long)l[0], (long)l[2]);
     for (int64_t n : {(int64_t)1, kRows, (int64_t)1 << 60})
-        if (gsz_dropout(p, p, p, n, GSZ_TYPE_F32, 0.5, (uint64_t*)p, 0, nullptr) != GSZ_OK && ++bad) std::printf("dropout of %ld refused\n", (long)n);
+        if (gsz_dropout(at(61), at(61), at(61), n, GSZ_TYPE_F32, 0.5, (uint64_t*)p, 0, nullptr) != GSZ_OK && ++bad) std::printf("dropout of %ld refused\n", (long)n);
+    // Buffers side by side: 16 values; 200 tokens on 10 rows of 8.
+    char* const b = static_cast<char*>(at(30));
+    size_t bytes = 0;
+    gsz_embedding_workspace_bytes(200, 10, 8, &bytes);
+    const bool taken =
+        gsz_dropout(b, b + 64, b + 32, 16, GSZ_TYPE_BF16, 0.5, (uint64_t*)(b + 96), 0, nullptr) == GSZ_OK &&
+        gsz_dropout(b + 64, b, b + 32, 16, GSZ_TYPE_BF16, 0.5, (uint64_t*)(b - 16), 0, nullptr) == GSZ_OK &&
+        gsz_dropout(b, b + 32, b + 32, 16, GSZ_TYPE_BF16, 0.5, (uint64_t*)(b + 64), 0, nullptr) == GSZ_OK &&
+        gsz_dropout(b, b + 2, b, 16, GSZ_TYPE_BF16, 0.0, (uint64_t*)b, 0, nullptr) == GSZ_ERR_INVALID_ARG &&
+        gsz_embedding_lookup(b, GSZ_TYPE_BF16, 10, 8, b + 160 + 64, GSZ_TYPE_I64, 4, 1.0, 0.5, (uint64_t*)(b + 256), 0, b + 160, GSZ_TYPE_BF16, nullptr) == GSZ_OK &&
+        gsz_embedding_grad(b, GSZ_TYPE_I64, 200, b + 1760, GSZ_TYPE_BF16, 10, 8, 1.0, 0.0, (uint64_t*)(b + 1600), 0, b + 1600, GSZ_TYPE_BF16, 0,
+                           b + 4960, bytes, nullptr) == GSZ_OK &&
+        gsz_embedding_grad(b, GSZ_TYPE_I64, 4, b + 32, GSZ_TYPE_BF16, 10, 8, 1.0, 0.0, nullptr, 0, b + 96, GSZ_TYPE_BF16, 0, b, 8, nullptr) == GSZ_OK;
+    if (!taken && ++bad) std::printf("buffers that only touch, or are not read, refused\n");
     return bad ? 1 : 0;
 }
 
