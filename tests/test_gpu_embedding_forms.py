@@ -46,3 +46,93 @@ def test_a_table_of_as_many_rows_as_there_may_be(n):
     assert int((grad != 0).sum()) == at.size
     del grad, ws
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_dropout_past_32_bits(dtype):
+    """2^32 + 5003 elements: places on both sides of 2^32 keep and drop what the
+    generator says and hold the kept values exactly doubled."""
+    n = (1 << 32) + 5003
+    x = torch.full((n,), 1.5, dtype=dtype, device="cuda")
+    x[-5003:] = torch.arange(1, 5004, device="cuda").remainder(64).add(1).to(dtype)
+    G.dropout(x, x, 0.5, rng_tensor(), SITE)
+    for first, m in ((0, 4099), ((1 << 31) - 2000, 4000), ((1 << 32) - 3000, 8003)):
+        kept = E.kept(first, m, 0.5, SEED, STEP, SITE)
+        e = np.arange(first, first + m)
+        was = np.where(e < 1 << 32, 1.5, (e - (1 << 32) + 1) % 64 + 1.0)
+        assert 0.4 < kept.mean() < 0.6
+        assert np.array_equal(f64(x[first:first + m]), np.where(kept, 2 * was, 0.0)), first
+    del x
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("p", [0.0, 0.5])
+@pytest.mark.parametrize("dim", [65_544, 65_541])
+def test_lookup_past_32_bits(dim, p):
+    """Rows of the table and of out on both sides of element 2^32, all of them full of
+    values, against the oracle's mask and an exact doubling."""
+    n, rows = 65_600, 65_700
+    ids = (torch.arange(n, device="cuda") * 7919) % rows
+    table = torch.empty(rows, dim, dtype=BF, device="cuda")
+    table.copy_(torch.arange(rows, device="cuda").remainder(61).add(1)[:, None].expand(rows, dim))
+    table += torch.arange(dim, device="cuda").remainder(2).to(BF)          # odd columns one more
+    out = torch.full((n, dim), float("nan"), dtype=BF, device="cuda")
+    G.embedding_lookup(ids, table, out, scale=2.0, p=p, rng=rng_tensor(), site=SITE)
+    k = 2.0 * E.keep_scale(p)
+    border = (1 << 32) // dim
+    far = int((ids > border).nonzero()[0, 0])
+    for i in (0, 1, far, border - 1, border, border + 1, n - 1):
+        kept = E.kept(i * dim, dim, p, SEED, STEP, SITE)
+        want = np.where(kept, (int(ids[i]) % 61 + 1 + np.arange(dim) % 2) * k, 0.0)
+        assert want.any() and np.array_equal(f64(out[i]), want), (i, int(ids[i]))
+    assert bool(torch.isfinite(out).all())
+    del table, out
+    torch.cuda.empty_cache()
+
+
+# A lane takes two vectors of 8 columns from 2^21 vectors in the call on, four from 2^22
+# on; rows lie side by side in a block up to 128 vectors, and longer ones are cut into
+# pieces of at most 256.
+@pytest.mark.parametrize("n,dim", [(2_200_003, 1), (4_200_003, 1), (1_100_003, 9), (300_007, 100), (33_001, 1016), (33_001, 1030),
+                                   (17_001, 2060), (11_003, 2048), (5601, 6150), (2207, 8200), (4241, 8193)])
+@pytest.mark.parametrize("tt,ot,it", [(BF, BF, torch.int64), (F32, BF, torch.int32), (BF, F32, torch.int32), (F32, F32, torch.int64)])
+def test_lookup_of_several_vectors_a_lane(n, dim, tt, ot, it):
+    """Every value of large lookups, from and to odd places, against the table's rows
+    doubled (exact in each type)."""
+    assert n * (-(-dim // 8)) >= 1 << 21
+    rows, shift = 1009, 3
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    tbuf = torch.randn(rows * dim + shift, device="cuda", generator=gen).to(BF).to(tt)
+    table = tbuf[shift:].view(rows, dim)
+    ids = torch.randint(-3, rows + 3, (n,), device="cuda", generator=gen).to(it)
+    obuf = torch.full((n * dim + shift + 8,), float("nan"), dtype=ot, device="cuda")
+    obuf[:shift], obuf[shift + n * dim:] = 7.25, 7.25
+    out = obuf[shift:shift + n * dim].view(n, dim)
+    G.embedding_lookup(ids, table, out, scale=2.0)
+    ok = (ids >= 0) & (ids < rows)
+    want = (table * 2).to(ot).index_select(0, ids.clamp(0, rows - 1).long())
+    want[~ok] = 0
+    assert torch.equal(out, want)
+    assert bool((obuf[:shift] == 7.25).all()) and bool((obuf[shift + n * dim:] == 7.25).all()), "wrote outside"
+
+
+@pytest.mark.parametrize("rows", [(1 << 19) - 1, 1 << 19, 600_001])
+@pytest.mark.parametrize("n", [129, 700, 8191, 8192])
+@pytest.mark.parametrize("acc,kind", [(False, "any"), (True, "any"), (False, "hot"), (True, "ends")])
+def test_grad_of_some_tokens_on_tall_tables(rows, n, acc, kind):
+    """The compare-all sort where a row's number and a token's position just fit, or do
+    not fit, one 32-bit key."""
+    dim = 3
+    rng = np.random.default_rng(rows + n)
+    i = np.where(rng.random(n) < 0.5, rows - 1, rng.choice([0, rows - 2, rows, -1], n)) if kind == "ends" else make_ids(kind, n, rows, rng)
+    i[:2] = rows - 1, rows
+    ids, dy = torch.from_numpy(i).cuda(), draw(rng, (n, dim), F32)
+    old = draw(rng, (rows, dim), F32)
+    grad = old.clone() if acc else torch.full_like(old, float("nan"))
+    ws = torch.full((G.embedding_workspace_bytes(n, rows, dim) // 4,), float("nan"), device="cuda")
+    G.embedding_grad(ids, dy, grad, ws, scale=0.5, accumulate=acc)
+    ref, size = E.grad(i, f64(dy), rows, 0.5, old=f64(old) if acc else None)
+    m = np.bincount(i[(i >= 0) & (i < rows)], minlength=rows).astype(float)[:, None]
+    near(grad, ref, size * ((1 + EPS) ** (m + 3) - 1) * (1 + EPS) ** 2 + out_bound(ref, F32, 1), (rows, n, kind))
+    rest = torch.from_numpy(m[:, 0] == 0).cuda()
+    assert torch.equal(grad[rest], old[rest] if acc else torch.zeros_like(old[rest]))
