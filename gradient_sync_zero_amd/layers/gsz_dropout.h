@@ -286,7 +286,7 @@ __device__ __forceinline__ uint32_t dropped_row(const DropKey& d, uint64_t first
 // many in 490 us (6.57 TB/s; 2 GiB copied by torch: 4.9), 48 Mi fp32 from an odd place in 64 us
 // (6.3 TB/s; with each lane's 8 values in a row, half a line an access, 74).  One wave per
 // block; four took 507 us.  A whole 32-bit word per element would take twice the products.
-constexpr int kDropBlock = 64, kDropTile = kDropBlock / 64 * kTile;
+constexpr int kDropBlock = 64;
 template <typename T, bool ADD, bool DROP, bool FULL>
 __device__ __forceinline__ void dropout_tile(const T* x, const T* add, T* y, int64_t e, int64_t left,
                                              float k, const DropKey& d) {
@@ -317,9 +317,8 @@ __global__ __launch_bounds__(kDropBlock) void k_dropout(const T* x, const T* add
                                                         float k, DropArgs da) {
     DropKey d{};
     if (DROP) d = drop_key(da);                      // rng may be NULL otherwise
-    const int64_t stride = (int64_t)gridDim.x * kDropTile;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    for (int64_t e = (int64_t)blockIdx.x * kDropTile + wave * kTile; e < n; e += stride) {
+    const int64_t stride = (int64_t)gridDim.x * kTile;
+    for (int64_t e = (int64_t)blockIdx.x * kTile; e < n; e += stride) {
         if (n - e >= kTile) dropout_tile<T, ADD, DROP, true>(x, add, y, e, n - e, k, d);
         else dropout_tile<T, ADD, DROP, false>(x, add, y, e, n - e, k, d);
     }

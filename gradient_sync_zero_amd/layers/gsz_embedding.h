@@ -281,7 +281,7 @@ __global__ __launch_bounds__(kRankBlock) void k_rank(Ids ids, int n, uint32_t* _
 // while placing this one, with an atomic per token where it lands, saved a launch and cost
 // 10 us of atomics on 16 Ki tokens.
 constexpr int kSortWaves = kSortBlock / 64, kSortMaxBins = 1024;
-constexpr int kSortPer = 1, kSortTile = kSortBlock * kSortPer;
+constexpr int kSortTile = kSortBlock;
 constexpr int kSortBinsPer = kSortMaxBins / kSortBlock;
 struct SortPass {
     Ids ids;                              // the tokens themselves (FIRST),
@@ -308,28 +308,19 @@ __global__ __launch_bounds__(kSortBlock) void k_count(SortPass s, uint32_t* __re
     for (int b = threadIdx.x; b < s.bins; b += kSortBlock) h[b] = 0;
     __syncthreads();
     for (int64_t r = 0; r < s.rounds; ++r) {
-        const int64_t i0 = (blockIdx.x * s.rounds + r) * kSortTile + threadIdx.x;
-        uint32_t k[kSortPer];
-#pragma unroll
-        for (int u = 0; u < kSortPer; ++u) {
-            const int64_t i = i0 + u * kSortBlock;
-            if (i < s.n) k[u] = FIRST ? row_of(s.ids, i) : s.key_in[i];
-        }
-#pragma unroll
-        for (int u = 0; u < kSortPer; ++u) {
-            const int64_t i = i0 + u * kSortBlock;
-            if (i >= s.n) continue;
-            atomicAdd(&h[digit_of(s, k[u])], 1u);
-            if (FIRST && owner && k[u] != s.ids.rows) owner[k[u]] = (uint32_t)i;
-        }
+        const int64_t i = (blockIdx.x * s.rounds + r) * kSortTile + threadIdx.x;
+        if (i >= s.n) continue;
+        const uint32_t k = FIRST ? row_of(s.ids, i) : s.key_in[i];
+        atomicAdd(&h[digit_of(s, k)], 1u);
+        if (FIRST && owner && k != s.ids.rows) owner[k] = (uint32_t)i;
     }
     __syncthreads();
     for (int b = threadIdx.x; b < s.bins; b += kSortBlock) count[(int64_t)blockIdx.x * s.bins + b] = h[b];
 }
 
 // Moves the tokens of one tile to their places by one digit.  The block sums the
-// digit counts of all tiles for its bases; in each round wave w counts its kSortPer * 64
-// tokens, then places them in order from its own bases.
+// digit counts of all tiles for its bases; in each round wave w counts its 64 tokens, then
+// places them in order from its own bases.
 template <bool FIRST>
 __global__ __launch_bounds__(kSortBlock) void k_place(SortPass s, const uint32_t* __restrict__ count,
                                                       uint32_t* __restrict__ key, uint32_t* __restrict__ pos,
@@ -375,23 +366,17 @@ __global__ __launch_bounds__(kSortBlock) void k_place(SortPass s, const uint32_t
         __syncthreads();
     }
     for (int64_t r = 0; r < s.rounds; ++r) {
-        // Wave w's tokens: kSortPer times 64 in a row.
-        const int64_t i0 = ((blockIdx.x * s.rounds + r) * kSortWaves + wave) * (64 * kSortPer) + lane;
-        uint32_t k[kSortPer], p[kSortPer];
-#pragma unroll
-        for (int u = 0; u < kSortPer; ++u) {
-            const int64_t i = i0 + 64 * u;
-            k[u] = p[u] = 0;
-            if (i < s.n) {
-                k[u] = FIRST ? row_of(s.ids, i) : s.key_in[i];
-                p[u] = FIRST ? (uint32_t)i : s.pos_in[i];
-            }
+        const int64_t i = (blockIdx.x * s.rounds + r) * kSortTile + tid;
+        const bool in = i < s.n;
+        uint32_t k = 0, p = 0;
+        if (in) {
+            k = FIRST ? row_of(s.ids, i) : s.key_in[i];
+            p = FIRST ? (uint32_t)i : s.pos_in[i];
         }
+        const uint32_t dg = digit_of(s, k);
         for (int b = lane; b < s.bins; b += 64) base[wave][b] = 0;
         wave_fence();
-#pragma unroll
-        for (int u = 0; u < kSortPer; ++u)
-            if (i0 + 64 * u < s.n) atomicAdd(&base[wave][digit_of(s, k[u])], 1u);
+        if (in) atomicAdd(&base[wave][dg], 1u);
         __syncthreads();
         for (int b = tid; b < s.bins; b += kSortBlock) {
             uint32_t at = next[b];
@@ -404,23 +389,17 @@ __global__ __launch_bounds__(kSortBlock) void k_place(SortPass s, const uint32_t
             next[b] = at;
         }
         __syncthreads();
-#pragma unroll
-        for (int u = 0; u < kSortPer; ++u) {
-            const bool in = i0 + 64 * u < s.n;
-            const uint32_t dg = digit_of(s, k[u]);
-            uint64_t same = __ballot(in);             // the lanes with this one's digit
-            for (int bit = 1; bit < s.bins; bit <<= 1) {
-                const uint64_t m = __ballot((dg & bit) != 0);
-                same &= (dg & bit) ? m : ~m;
-            }
-            const uint32_t rank = __popcll(same & (((uint64_t)1 << lane) - 1));
-            uint32_t at = 0;
-            if (in) at = base[wave][dg] + rank;
-            wave_fence();
-            if (in && rank == 0) base[wave][dg] = at + __popcll(same);
-            wave_fence();
-            if (in) { key[at] = k[u]; pos[at] = p[u]; }
+        uint64_t same = __ballot(in);                 // the lanes with this one's digit
+        for (int bit = 1; bit < s.bins; bit <<= 1) {
+            const uint64_t m = __ballot((dg & bit) != 0);
+            same &= (dg & bit) ? m : ~m;
         }
+        if (in) {
+            const uint32_t at = base[wave][dg] + __popcll(same & (((uint64_t)1 << lane) - 1));
+            key[at] = k;
+            pos[at] = p;
+        }
+        wave_fence();                                 // before the next round clears base
     }
 }
 
@@ -442,7 +421,7 @@ __global__ __launch_bounds__(kSortBlock) void k_place(SortPass s, const uint32_t
 // the counters, 5.0 TB/s).  One wave per block and four rows in flight beat four waves by
 // 2-5% and eight rows by 0-4%.
 
-constexpr int kGradBlock = 64, kGradWaves = kGradBlock / 64, kGradCols = kTile, kGradUnroll = 4;
+constexpr int kGradBlock = 64, kGradCols = kTile, kGradUnroll = 4;
 constexpr int kMaxChunk = 32;                         // a wave holds 2 K keys
 
 struct GradShape {
@@ -518,10 +497,9 @@ __global__ __launch_bounds__(kGradBlock) void k_grad(const T* __restrict__ dy, c
                                                      float c0, DropArgs da, G* __restrict__ grad,
                                                      float* __restrict__ part) {
     const int lane = threadIdx.x & 63;
-    const int64_t wave = (int64_t)blockIdx.x * kGradWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t chunk = wave / s.tiles;
+    const int64_t chunk = (int64_t)blockIdx.x / s.tiles;
     if (chunk >= s.chunks) return;
-    const int64_t c = (wave - chunk * s.tiles) * kGradCols;
+    const int64_t c = ((int64_t)blockIdx.x - chunk * s.tiles) * kGradCols;
     const int64_t s0 = chunk * s.K, s1 = s0 + s.K;
     // Lane l holds the key and position of token s0 + l, l < 2 K.
     uint32_t my_key = s.rows, my_pos = 0;
@@ -665,10 +643,9 @@ __global__ __launch_bounds__(kGradBlock) void k_direct(const T* __restrict__ dy,
         }
         return;
     }
-    const int64_t w = (int64_t)blockIdx.x * kGradWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int i = (int)(w / s.tiles);
+    const int i = (int)((int64_t)blockIdx.x / s.tiles);
     if (i >= s.n) return;
-    const int64_t c = (w - (int64_t)i * s.tiles) * kGradCols, left = s.dim - c;
+    const int64_t c = ((int64_t)blockIdx.x - (int64_t)i * s.tiles) * kGradCols, left = s.dim - c;
     const uint32_t mine = i < 64 ? __builtin_amdgcn_readlane(k0, i) : __builtin_amdgcn_readlane(k1, i - 64);
     uint64_t m0 = __ballot(k0 == mine), m1 = __ballot(k1 == mine);
     if (mine == s.rows || (m0 ? __builtin_ctzll(m0) : 64 + __builtin_ctzll(m1)) != i) return;

@@ -187,7 +187,7 @@ extern "C" int gsz_dropout(const void* x, const void* add, void* y, int64_t n, i
         return bad_arg(who, "y overlaps x, add or rng");
     if ((rc = check_device(who))) return rc;
     if (n == 0) return GSZ_OK;
-    const int grid = grid_for((n + kDropTile - 1) / kDropTile, kDropBlock);
+    const int grid = grid_for((n + kTile - 1) / kTile, kDropBlock);
     with_type(type, [&](auto t) {
         using T = decltype(t);
         with_bool(add != nullptr, [&](auto a) {
@@ -317,7 +317,7 @@ extern "C" int gsz_embedding_grad(const void* ids, int32_t id_type, int64_t n, c
     auto clear_for = [&] { return accumulate ? 0 : (rows + (int64_t)per * (rank ? 64 : 1) - 1) / ((int64_t)per * (rank ? 64 : 1)); };
     while (rank && per < 64 && clear_for() > rank_max) per *= 2;
     int64_t clear_blocks = clear_for();                              // the other sort divides them over its launches
-    const int64_t sum_blocks = ((direct ? n : g.chunks) * g.tiles + kGradWaves - 1) / kGradWaves;
+    const int64_t sum_blocks = (direct ? n : g.chunks) * g.tiles;
     if (direct && clear_blocks > 0 && clear_blocks > direct_max - sum_blocks)
         clear_blocks = direct_max > sum_blocks ? direct_max - sum_blocks : 1;
     const int join_tiles = (int)((dim + kJoinCols - 1) / kJoinCols);
