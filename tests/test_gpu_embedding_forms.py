@@ -136,3 +136,38 @@ def test_grad_of_some_tokens_on_tall_tables(rows, n, acc, kind):
     near(grad, ref, size * ((1 + EPS) ** (m + 3) - 1) * (1 + EPS) ** 2 + out_bound(ref, F32, 1), (rows, n, kind))
     rest = torch.from_numpy(m[:, 0] == 0).cuda()
     assert torch.equal(grad[rest], old[rest] if acc else torch.zeros_like(old[rest]))
+
+
+def test_grad_of_as_many_tokens_as_there_may_be():
+    """2^30 tokens (the sort's tiles go over 8192 rounds each), small whole numbers, about
+    1074 tokens a row: every sum is exact in fp32."""
+    n, rows = 1 << 30, 1_000_003
+    ids = torch.arange(n, dtype=torch.int32, device="cuda").remainder_(rows)
+    dy = torch.arange(n, dtype=torch.int32, device="cuda").bitwise_right_shift_(7).remainder_(5).to(BF).view(n, 1)
+    grad = torch.full((rows, 1), float("nan"), device="cuda")
+    ws = torch.empty(G.embedding_workspace_bytes(n, rows, 1), dtype=torch.uint8, device="cuda")
+    G.embedding_grad(ids, dy, grad, ws)
+    want = torch.zeros(rows, dtype=torch.float64, device="cuda")
+    for a in range(0, n, 1 << 27):
+        want.index_add_(0, ids[a:a + (1 << 27)].long(), dy[a:a + (1 << 27), 0].double())
+    assert float(want.max()) < 1 << 24 and torch.equal(grad[:, 0].double(), want)
+    del ids, dy, ws, want
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dim", [1 << 29, (1 << 29) - 3])
+def test_rows_as_wide_as_they_may_be(dim):
+    """2^29 columns and three fewer: lookup, and the gradient of its three tokens."""
+    table = torch.empty(2, dim, dtype=BF, device="cuda")
+    for r in range(2):
+        table[r] = torch.arange(dim, dtype=torch.int32, device="cuda").remainder_(251 - r).to(BF)
+    ids = torch.tensor([1, 2, 1], device="cuda")
+    out = torch.full((3, dim), float("nan"), dtype=BF, device="cuda")
+    G.embedding_lookup(ids, table, out, scale=2.0)
+    assert torch.equal(out[0], table[1] * 2) and torch.equal(out[2], out[0]) and not bool(out[1].any())
+    out[1] = 9.0
+    grad = torch.full((2, dim), float("nan"), dtype=BF, device="cuda")
+    G.embedding_grad(ids, out, grad, None, scale=0.25)
+    assert torch.equal(grad[1], table[1]) and not bool(grad[0].any())
+    del table, out, grad
+    torch.cuda.empty_cache()
