@@ -442,7 +442,9 @@ int gsz_embedding_workspace_bytes(int64_t n, int64_t rows, int64_t dim, size_t* 
  * alone: the same call gives the same bits.  One rounding to grad_type at the end.
  * accumulate = 0 writes every row (0 where no token has it); accumulate = 1 reads
  * and writes only the rows that tokens have, as gsz_bucket_accumulate[_f32] adds a
- * micro-batch to a bucket.  Ids outside [0, rows) add nothing.
+ * micro-batch to a bucket.  Ids outside [0, rows) add nothing.  (gsz_bucket_pack[_f32] and
+ * gsz_bucket_accumulate[_f32] write every tensor's place: they go before this call, with
+ * any tensor in the table's place when packing, zeros when accumulating.)
  *   dy (device, n * dim of dy_type); grad (device, rows * dim of grad_type): both any
  *     multiple of the value's size, so grad may be a tensor's place in a bf16 or fp32
  *     bucket-flat buffer.  It must not overlap dy or ids.

@@ -171,3 +171,31 @@ def test_rows_as_wide_as_they_may_be(dim):
     assert torch.equal(grad[1], table[1]) and not bool(grad[0].any())
     del table, out, grad
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("bucket", [BF, F32])
+def test_beside_the_calls_that_pack_every_tensor(bucket):
+    """The table's gradient in a bucket that bucket_pack and bucket_accumulate fill: those
+    write every tensor's place, so they go first, the table's place taking anything when
+    packed and zeros when accumulated."""
+    rows, dim, n = 300, 101, 500
+    rng = np.random.default_rng(9)
+    plan = G.Plan([rows * dim, 37, 5000], 1 << 16, 2).upload()
+    flat = torch.full((plan.flat_len,), float("nan"), dtype=bucket, device="cuda")
+    pack, add = (G.bucket_pack, G.bucket_accumulate) if bucket == BF else (G.bucket_pack_f32, G.bucket_accumulate_f32)
+    slot = plan.view(0, flat).view(rows, dim)
+    ws = torch.empty(G.embedding_workspace_bytes(n, rows, dim), dtype=torch.uint8, device="cuda")
+    total, others = None, [np.zeros(37), np.zeros(5000)]
+    for k in range(3):
+        fill = torch.zeros(rows * dim, dtype=BF, device="cuda") if k else draw(rng, rows * dim, BF)
+        rest = [torch.from_numpy(rng.integers(-8, 9, m).astype(np.float32)).to(BF).cuda() for m in (37, 5000)]
+        (add if k else pack)(plan, [fill, *rest], flat)
+        i = make_ids("any", n, rows, rng)
+        dy = torch.from_numpy(rng.integers(-2, 3, (n, dim)).astype(np.float32)).to(BF).cuda()
+        G.embedding_grad(torch.from_numpy(i).cuda(), dy, slot, ws, accumulate=k > 0)
+        total = E.grad(i, f64(dy), rows, old=total)[0]
+        others = [o + f64(r) for o, r in zip(others, rest)]
+    assert np.abs(total).max() <= 256                    # whole numbers that bf16 holds too
+    assert np.array_equal(f64(slot), total)
+    assert all(np.array_equal(f64(plan.view(t + 1, flat)), o) for t, o in enumerate(others))
+    assert bool(torch.isfinite(flat).all())              # the pads are zero

@@ -37,5 +37,5 @@ def test_random_cases_in_the_fewest_blocks(prog, op):
         return (seed, r.returncode, r.stdout[-2000:], r.stderr[-2000:])
 
     with concurrent.futures.ThreadPoolExecutor(4) as pool:
-        bad = [x for x in pool.map(run, range(1, 17)) if x[1] != 0]
+        bad = [x for x in pool.map(run, range(1, 11)) if x[1] != 0]
     assert not bad, bad[:2]
