@@ -57,6 +57,12 @@ class AdamWHP(ctypes.Structure):
                 ("step", ctypes.c_int64)]
 
 
+class MuonHP(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("scale", ctypes.c_double), ("eps", ctypes.c_double), ("ns", ctypes.POINTER(ctypes.c_double)),
+                ("steps", ctypes.c_int32), ("nesterov", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -92,6 +98,16 @@ _SIGS = {
     "gsz_embedding_workspace_bytes": [_I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
     "gsz_embedding_grad": [_P, _I32, _I64, _P, _I32, _I64, _I64, ctypes.c_double, ctypes.c_double,
                            _P, ctypes.c_uint32, _P, _I32, _I32, _P, ctypes.c_size_t, _P],
+    "gsz_muon_workspace_bytes": [_I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "gsz_orthogonalize": [_P, _I32, _I64, _I64, _I64, _I32, ctypes.POINTER(ctypes.c_double), ctypes.c_double,
+                          _P, _P, ctypes.c_size_t, _P],
+    "gsz_muon_step": [_P, ctypes.POINTER(_I32), _I32, _I64, _I64, _P, _P, _P, _P, ctypes.POINTER(MuonHP), _P, _P,
+                      ctypes.c_size_t, _P],
+    "gsz_relpos_bias": [_P, _I32, _I64, _I64, _I64, _I32, _I64, _I64, _I64, _I64, _P, _I32, ctypes.c_double,
+                        _P, _P, _I32, _P],
+    "gsz_relpos_bias_workspace_bytes": [_I64, _I64, _I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "gsz_relpos_bias_grad": [_P, _I32, _I64, _I64, _I64, _I32, _I64, _I64, _I64, _I64, _P, _I32, ctypes.c_double,
+                             _P, _I32, _I32, _P, ctypes.c_size_t, _P],
 }
 
 _TEST_SIGS = {"gsz_test_set_grid_limit": [ctypes.c_int64],
@@ -698,5 +714,152 @@ def embedding_grad(ids, dy, grad, ws, scale=1.0, p=0.0, rng=None, site=0, accumu
     lib = load()
     rc = lib.gsz_embedding_grad(ip, it, n, dp, dt, rows, dim, scale, p, rp, site, gp, gt,
                                 1 if accumulate else 0, wp, nbytes, _layer_stream(stream, dev))
+    if rc:
+        _check(rc, lib)
+
+
+def muon_workspace_bytes(count, rows, cols):
+    """Device scratch bytes for orthogonalize or muon_step of `count` matrices of rows x cols, or
+    fewer."""
+    out = ctypes.c_size_t()
+    _check(load().gsz_muon_workspace_bytes(int(count), int(rows), int(cols), ctypes.byref(out)))
+    return out.value
+
+
+def _coefficients(ns, steps):
+    """Host array of the steps' (a, b, c), or None for the usual ones."""
+    if ns is None:
+        return None
+    flat = [float(v) for step in ns for v in step]
+    if len(ns) != steps or len(flat) != 3 * steps:
+        raise ValueError(f"ns holds {len(ns)} steps, the call takes {steps} of three coefficients each")
+    return (ctypes.c_double * len(flat))(*flat)
+
+
+def _workspace(ws, dev):
+    """(address, bytes) of a workspace tensor on device dev, or of none."""
+    if ws is None:
+        return None, 0
+    return _arg(ws, "ws", {ws.dtype: 0}, "", None, dev)[1], ws.numel() * ws.element_size()
+
+
+def orthogonalize(x, out, ws, steps=5, ns=None, eps=1e-7, stream=None):
+    """gsz_orthogonalize: Newton-Schulz on each matrix of x, (rows, cols) or (count, rows, cols) in
+    bf16 or fp32, to out, bf16 (x itself if that is bf16).  ns: (a, b, c) for each step, or None.
+    ws: a tensor of at least muon_workspace_bytes(count, rows, cols)."""
+    if not _VALUES:
+        _fill_types()
+    if x is None or x.dim() not in (2, 3):
+        raise ValueError("x must be a 2-D or 3-D tensor ([count,] rows, cols)")
+    count, rows, cols = (1, *x.shape) if x.dim() == 2 else x.shape
+    ty, xp, dev = _value(x, "x")
+    ot, op, _ = _value(out, "out", x.numel(), dev)
+    if ot != 0:
+        raise ValueError(f"out has dtype {out.dtype}, expected bf16 (or its bits)")
+    wp, nbytes = _workspace(ws, dev)
+    lib = load()
+    rc = lib.gsz_orthogonalize(xp, ty, count, rows, cols, steps, _coefficients(ns, steps), eps, op, wp, nbytes,
+                               _layer_stream(stream, dev))
+    if rc:
+        _check(rc, lib)
+
+
+def make_muon_hp(lr, momentum=0.95, weight_decay=0.0, scale=1.0, nesterov=True, steps=5, ns=None, eps=1e-7):
+    """Hyperparameters of muon_step; scale multiplies the orthogonalised update (0.2 sqrt(max(rows,
+    cols)) gives it the size of an AdamW update), ns as orthogonalize's."""
+    hp = MuonHP(lr, momentum, weight_decay, scale, eps, None, steps, 1 if nesterov else 0)
+    if ns is not None:
+        hp.ns = _coefficients(ns, steps)            # the structure keeps the array alive
+    return hp
+
+
+def muon_step(plan, tensors, rows, cols, master, momentum, g, coef, hp, params, ws, stream=None):
+    """gsz_muon_step: the Muon update of the plan's `tensors` (forward indices, each rows x cols) in
+    place in the flat fp32 buffers master and momentum, g the flat gradient, params the flat bf16
+    parameters.  ws: a tensor of at least muon_workspace_bytes(len(tensors), rows, cols)."""
+    if not _VALUES:
+        _fill_types()
+    lib = _lib_for(plan)
+    count = len(tensors)
+    arr = (_I32 * max(count, 1))(*tensors)
+    f32, what, n = {master.dtype: 1}, "float32", plan.flat_len
+    if _VALUES.get(master.dtype) != 1:
+        raise ValueError(f"master has dtype {master.dtype}, expected float32")
+    _, wp, dev = _arg(master, "master", f32, what)
+    mp = _arg(momentum, "momentum", f32, what, None, dev)[1]
+    gp = _arg(g, "g", f32, what, None, dev)[1]
+    cp = _arg(coef, "coef", f32, what, None, dev)[1]
+    pt, pp, _ = _value(params, "params", None, dev)
+    if pt != 0:
+        raise ValueError(f"params has dtype {params.dtype}, expected bf16 (or its bits)")
+    for t, name, least in ((master, "master", n), (momentum, "momentum", n), (g, "g", n), (params, "params", n), (coef, "coef", 1)):
+        if t.numel() < least:
+            raise ValueError(f"{name} has {t.numel()} elements, the call needs at least {least}")
+    sp, nbytes = _workspace(ws, dev)
+    rc = lib.gsz_muon_step(plan.handle, arr, count, rows, cols, wp, mp, gp, cp, ctypes.byref(hp), pp, sp, nbytes,
+                           _layer_stream(stream, dev))
+    if rc:
+        _check(rc, lib)
+
+
+def _q_start(q_start, batch, dev):
+    """(number, address, type) of a common start or of a device tensor of one a sequence."""
+    if hasattr(q_start, "data_ptr"):
+        ty, p, _ = _arg(q_start, "q_start", _IDS, _I, batch, dev)
+        return 0, p, ty
+    return int(q_start), None, 0
+
+
+def _scores_shape(t, name, heads):
+    if t is None or t.dim() != 4:
+        raise ValueError(f"{name} must be a 4-D tensor (batch, heads, q_len, k_len)")
+    if t.shape[1] != heads:
+        raise ValueError(f"{name} has {t.shape[1]} heads, the table {heads}")
+    return t.shape
+
+
+def relpos_bias(table, out, max_distance, bidirectional=True, q_start=0, scale=1.0, add=None, stream=None):
+    """gsz_relpos_bias: out[n, h, i, j] = (add or 0) + scale * table[bucket(j - i - start), h].  table is
+    2-D (buckets, heads), for instance plan.view(t, gathered).view(buckets, heads); out and add are 4-D
+    (batch, heads, q_len, k_len).  q_start: a number, or a device tensor of one integer a sequence."""
+    if not _VALUES:
+        _fill_types()
+    buckets, heads = _table_shape(table, "table")
+    batch, _, q, k = _scores_shape(out, "out", heads)
+    tt, tp, dev = _value(table, "table")
+    ot, op, _ = _value(out, "out", None, dev)
+    ap = None if add is None else _arg(add, "add", {out.dtype: ot}, "out's", out.numel(), dev)[1]
+    start, sp, st = _q_start(q_start, batch, dev)
+    lib = load()
+    rc = lib.gsz_relpos_bias(tp, tt, buckets, heads, max_distance, 1 if bidirectional else 0, batch, q, k, start, sp, st,
+                             scale, ap, op, ot, _layer_stream(stream, dev))
+    if rc:
+        _check(rc, lib)
+
+
+def relpos_bias_workspace_bytes(batch, heads, q_len, k_len, buckets):
+    """Device scratch bytes for relpos_bias_grad of these sizes."""
+    out = ctypes.c_size_t()
+    _check(load().gsz_relpos_bias_workspace_bytes(int(batch), int(heads), int(q_len), int(k_len), int(buckets),
+                                                  ctypes.byref(out)))
+    return out.value
+
+
+def relpos_bias_grad(dy, grad, ws, max_distance, bidirectional=True, q_start=0, scale=1.0, accumulate=False, stream=None):
+    """gsz_relpos_bias_grad: the gradient of relpos_bias (same max_distance, bidirectional, q_start and
+    scale) with respect to its table, written to grad (2-D, buckets x heads; for instance plan.view(t,
+    flat).view(buckets, heads) of a bucket buffer) or, with accumulate, added to it.  dy: 4-D (batch,
+    heads, q_len, k_len).  ws: a tensor of at least relpos_bias_workspace_bytes."""
+    if not _VALUES:
+        _fill_types()
+    buckets, heads = _table_shape(grad, "grad")
+    batch, _, q, k = _scores_shape(dy, "dy", heads)
+    gt, gp, dev = _value(grad, "grad")
+    dt, dp, _ = _value(dy, "dy", None, dev)
+    start, sp, st = _q_start(q_start, batch, dev)
+    wp, nbytes = _workspace(ws, dev)
+    lib = load()
+    rc = lib.gsz_relpos_bias_grad(dp, dt, buckets, heads, max_distance, 1 if bidirectional else 0, batch, q, k, start, sp,
+                                  st, scale, gp, gt, 1 if accumulate else 0, wp, nbytes, _layer_stream(stream, dev))
     if rc:
         _check(rc, lib)

@@ -1,0 +1,322 @@
+// Host half of the orthogonalising entry points of include/gsz.h: argument checks, launch
+// shapes, workspace layout.  The kernels are in gsz_muon.h and gsz_product.h.
+#pragma clang fp contract(off)
+
+#include <hip/hip_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstring>
+#include <type_traits>
+#include <vector>
+
+#include "gsz_muon.h"
+
+using gsz::set_error;
+
+namespace {
+
+int hip_fail(const char* who, hipError_t e) {
+    set_error("%s: %s", who, hipGetErrorString(e));
+    return GSZ_ERR_HIP;
+}
+
+// GSZ_OK where the current device is gfx950.
+int check_device(const char* who) {
+    static std::atomic<int> known[64];               // 0 unknown, 1 gfx950, -1 other
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(who, e);
+    if (dev < 0 || dev >= 64) { set_error("%s: device index %d unsupported", who, dev); return GSZ_ERR_DEVICE; }
+    int st = known[dev].load();
+    if (st == 0) {
+        hipDeviceProp_t prop;
+        e = hipGetDeviceProperties(&prop, dev);
+        if (e != hipSuccess) return hip_fail(who, e);
+        st = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : -1;
+        known[dev].store(st);
+    }
+    if (st != 1) { set_error("%s: device %d is not gfx950 (MI355X); this library targets gfx950 only", who, dev); return GSZ_ERR_DEVICE; }
+    return GSZ_OK;
+}
+
+int launched(const char* who) {
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? (int)GSZ_OK : hip_fail(who, e);
+}
+
+int bad_arg(const char* who, const char* what) {
+    set_error("%s: %s", who, what);
+    return GSZ_ERR_INVALID_ARG;
+}
+
+int64_t value_size(int32_t type) { return type == GSZ_TYPE_BF16 ? 2 : type == GSZ_TYPE_F32 ? 4 : 0; }
+bool off_by(const void* p, int64_t align) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)align != 0; }
+
+struct Span { const void* p; int64_t bytes; };
+bool overlap(Span a, Span b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && (x < y ? y - x < (uintptr_t)a.bytes : x - y < (uintptr_t)b.bytes);
+}
+
+constexpr int64_t kMostSide = (int64_t)1 << 17, kMostElements = (int64_t)1 << 32;
+
+int check_shape(const char* who, int64_t count, int64_t rows, int64_t cols) {
+    if (count < 0 || rows < 0 || cols < 0) return bad_arg(who, "negative size");
+    if (rows > kMostSide || cols > kMostSide || rows * cols > kMostElements || count > (int64_t)1 << 31) {
+        set_error("%s: count %lld, rows %lld or cols %lld over the limits 2^31, 2^17, 2^17 or 2^32 elements a matrix", who,
+                  (long long)count, (long long)rows, (long long)cols);
+        return GSZ_ERR_SIZE;
+    }
+    return GSZ_OK;
+}
+
+int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+// How a call of `count` matrices goes: in groups of at most kMuonBatch, with tiles of one size.
+struct Shape {
+    int64_t rows, cols, small, large;            // as given; the smaller and the larger side, padded
+    int64_t padded_rows, padded_cols, norm_tiles;
+    int tile;
+    bool tall;
+};
+Shape shape_for(int64_t rows, int64_t cols, int tile) {
+    Shape s{};
+    s.rows = rows;
+    s.cols = cols;
+    s.tile = tile;
+    s.tall = rows > cols;
+    s.padded_rows = up(rows, tile);
+    s.padded_cols = up(cols, tile);
+    s.small = s.tall ? s.padded_cols : s.padded_rows;
+    s.large = s.tall ? s.padded_rows : s.padded_cols;
+    s.norm_tiles = (rows * cols + kNormTile - 1) / kNormTile;
+    return s;
+}
+
+int tile_for(int64_t group, int64_t rows, int64_t cols) {
+    const int64_t big = group * (up(rows, 256) / 256) * (up(cols, 256) / 256);
+    return big >= 200 ? 256 : 128;
+}
+
+int64_t group_of(int64_t count) { return count < kMuonBatch ? count : kMuonBatch; }
+
+struct Workspace { size_t partial, scale, x[2], a, s, bytes; };
+Workspace workspace_for(int64_t group, const Shape& s) {
+    Workspace w{};
+    size_t at = 0;
+    auto take = [&](size_t bytes) { const size_t o = at; at += (bytes + 255) / 256 * 256; return o; };
+    w.partial = take((size_t)8 * group * s.norm_tiles);
+    w.scale = take((size_t)8 * group);
+    for (int k = 0; k < 2; ++k) w.x[k] = take((size_t)2 * group * s.small * s.large);
+    w.a = take((size_t)2 * group * s.small * s.small);
+    w.s = take((size_t)2 * group * s.small * s.small);
+    w.bytes = at;
+    return w;
+}
+
+template <int T> struct Waves;
+template <> struct Waves<256> { static constexpr int m = 2, n = 4; };
+template <> struct Waves<128> { static constexpr int m = 2, n = 2; };
+
+// One product over a group: C[i, j] = sum_k L[i, k] R[j, k], i < down * T, j < across * T.
+template <int T, bool TL, bool TR, class E>
+int product(const char* who, int64_t group, Operand L, Operand R, int64_t M, int64_t N, int64_t K, bool half, const E& e, hipStream_t stream) {
+    constexpr int WM = Waves<T>::m, WN = Waves<T>::n;
+    Tiles t{};
+    t.down = (int)(M / T);
+    t.across = (int)(N / T);
+    t.half = half;
+    t.per = half ? t.down * (t.down + 1) / 2 : t.down * t.across;
+    t.total = group * t.per;
+    hipLaunchKernelGGL((k_product<T, T, WM, WN, TL, TR, E>), dim3((unsigned)t.total), dim3(64 * WM * WN), 0, stream, L, R, M, N, K, t, e);
+    return launched(who);
+}
+
+// All steps of a group whose scaled matrices lie at w.x[0]; the last product goes to `last`.
+template <int T, class E>
+int newton_schulz(const char* who, int64_t group, const Shape& s, const Workspace& w, char* base, int steps, const double* ns, const E& last, hipStream_t stream) {
+    _Float16* A = reinterpret_cast<_Float16*>(base + w.a);
+    _Float16* S = reinterpret_cast<_Float16*>(base + w.s);
+    const int64_t size = s.small * s.large, square = s.small * s.small;
+    const Operand a{A, square, s.small}, p{S, square, s.small};
+    for (int k = 0; k < steps; ++k) {
+        const double* q = ns + 3 * k;
+        _Float16* in = reinterpret_cast<_Float16*>(base + w.x[k & 1]);
+        _Float16* out = reinterpret_cast<_Float16*>(base + w.x[~k & 1]);
+        const Operand x{in, size, s.padded_cols};
+        const StoreHalf<true> gram{A, square, s.small, kScaleA / (kScaleX * kScaleX)};
+        int rc = s.tall ? product<T, true, true>(who, group, x, x, s.small, s.small, s.large, true, gram, stream)
+                        : product<T, false, false>(who, group, x, x, s.small, s.small, s.large, true, gram, stream);
+        if (rc) return rc;
+        const StorePolynomial poly{A, S, square, s.small, (float)(q[0] * kScaleA), (float)q[1], (float)(q[2] / kScaleA)};
+        if ((rc = product<T, false, false>(who, group, a, a, s.small, s.small, s.small, true, poly, stream))) return rc;
+        auto apply = [&](const auto& e) {
+            return s.tall ? product<T, false, false>(who, group, x, p, s.large, s.small, s.small, false, e, stream)
+                          : product<T, false, true>(who, group, p, x, s.small, s.large, s.small, false, e, stream);
+        };
+        rc = k + 1 < steps ? apply(StoreHalf<false>{out, size, s.padded_cols, 1.0f / kScaleA}) : apply(last);
+        if (rc) return rc;
+    }
+    return GSZ_OK;
+}
+
+template <class F>
+int with_tile(int tile, F&& f) {
+    return tile == 256 ? f(std::integral_constant<int, 256>{}) : f(std::integral_constant<int, 128>{});
+}
+
+constexpr double kUsual[3] = {3.4445, -4.7750, 2.0315};
+constexpr int kMostSteps = 16;
+
+// The steps' coefficients: the caller's, or the usual ones for every step.
+int check_steps(const char* who, int32_t steps, const double* ns, double eps, double out[3 * kMostSteps]) {
+    if (steps < 1 || steps > kMostSteps) { set_error("%s: steps %d is not in [1, %d]", who, (int)steps, kMostSteps); return GSZ_ERR_INVALID_ARG; }
+    if (!(eps >= 1e-30 && eps <= 1e30)) { set_error("%s: eps %g is not in [1e-30, 1e30]", who, eps); return GSZ_ERR_INVALID_ARG; }
+    for (int k = 0; k < 3 * steps; ++k) {
+        out[k] = ns ? ns[k] : kUsual[k % 3];
+        if (!(std::fabs(out[k]) <= 1e4)) return bad_arg(who, "a coefficient is not within 1e4 of 0");
+    }
+    return GSZ_OK;
+}
+
+int check_workspace(const char* who, const void* ws, size_t have, size_t need) {
+    if (!ws || have < need) { set_error("%s: workspace of %zu bytes required", who, need); return GSZ_ERR_SIZE; }
+    if (off_by(ws, 16)) { set_error("%s: workspace is not 16-byte aligned", who); return GSZ_ERR_MISALIGNED; }
+    return GSZ_OK;
+}
+
+Padded padded(const Shape& s) { return Padded{s.rows, s.cols, s.padded_cols, s.padded_rows * s.padded_cols / 8}; }
+
+}  // namespace
+
+extern "C" int gsz_muon_workspace_bytes(int64_t count, int64_t rows, int64_t cols, size_t* out) {
+    const char* who = "gsz_muon_workspace_bytes";
+    const int rc = check_shape(who, count, rows, cols);
+    if (rc) return rc;
+    if (!out) return bad_arg(who, "NULL output");
+    *out = count && rows && cols ? workspace_for(group_of(count), shape_for(rows, cols, 256)).bytes : 0;
+    return GSZ_OK;
+}
+
+extern "C" int gsz_orthogonalize(const void* x, int32_t type, int64_t count, int64_t rows, int64_t cols, int32_t steps,
+                                 const double* ns, double eps, uint16_t* out, void* ws, size_t ws_bytes, hipStream_t stream) {
+    const char* who = "gsz_orthogonalize";
+    const int64_t size = value_size(type);
+    if (!size) return bad_arg(who, "unknown value type");
+    int rc = check_shape(who, count, rows, cols);
+    if (rc) return rc;
+    double q[3 * kMostSteps];
+    if ((rc = check_steps(who, steps, ns, eps, q))) return rc;
+    const int64_t n = rows * cols;
+    if (count == 0 || n == 0) return check_device(who);
+    if (!x || !out) return bad_arg(who, "NULL buffer");
+    if (off_by(x, size) || off_by(out, 2)) { set_error("%s: a buffer is not aligned to its values", who); return GSZ_ERR_MISALIGNED; }
+    const int64_t group = group_of(count);
+    const size_t need = workspace_for(group, shape_for(rows, cols, 256)).bytes;
+    if ((rc = check_workspace(who, ws, ws_bytes, need))) return rc;
+    const Span in{x, count * n * size}, written{out, count * n * 2}, scratch{ws, (int64_t)need};
+    if ((x != out || size != 2) && overlap(written, in)) return bad_arg(who, "out overlaps x");
+    if (overlap(scratch, in) || overlap(scratch, written)) return bad_arg(who, "ws overlaps x or out");
+    if ((rc = check_device(who))) return rc;
+
+    const Shape s = shape_for(rows, cols, tile_for(group, rows, cols));
+    const Workspace w = workspace_for(group, s);
+    char* base = static_cast<char*>(ws);
+    double* partial = reinterpret_cast<double*>(base + w.partial);
+    double* scale = reinterpret_cast<double*>(base + w.scale);
+    _Float16* x0 = reinterpret_cast<_Float16*>(base + w.x[0]);
+    const Padded p = padded(s);
+    const int64_t tiles = (p.vectors + kUpdateBlock - 1) / kUpdateBlock;
+    for (int64_t first = 0; first < count; first += kMuonBatch) {
+        const int64_t m = count - first < kMuonBatch ? count - first : kMuonBatch;
+        auto prepare = [&](auto t) {
+            using T = decltype(t);
+            const T* from = static_cast<const T*>(x) + first * n;
+            hipLaunchKernelGGL((k_norm<T>), dim3((unsigned)(m * s.norm_tiles)), dim3(kUpdateBlock), 0, stream, from, n, s.norm_tiles, partial);
+            if (int e = launched(who)) return e;
+            hipLaunchKernelGGL(k_scale, dim3((unsigned)m), dim3(kBlock), 0, stream, partial, s.norm_tiles, eps, scale);
+            if (int e = launched(who)) return e;
+            hipLaunchKernelGGL((k_scaled<T>), dim3((unsigned)(m * tiles)), dim3(kUpdateBlock), 0, stream, from, p, tiles, scale, x0);
+            return launched(who);
+        };
+        rc = size == 2 ? prepare(uint16_t{}) : prepare(float{});
+        if (rc) return rc;
+        const StoreResult last{out + first * n, rows, cols, 1.0f / (kScaleA * kScaleX)};
+        rc = with_tile(s.tile, [&](auto t) { return newton_schulz<decltype(t)::value>(who, m, s, w, base, steps, q, last, stream); });
+        if (rc) return rc;
+    }
+    return GSZ_OK;
+}
+
+extern "C" int gsz_muon_step(const gsz_plan* plan, const int32_t* tensors, int32_t count, int64_t rows, int64_t cols,
+                             float* master, float* momentum, const float* g, const float* coef, const gsz_muon_hp* hp,
+                             uint16_t* params, void* ws, size_t ws_bytes, hipStream_t stream) {
+    const char* who = "gsz_muon_step";
+    if (!plan || !hp) return bad_arg(who, "plan or hp is NULL");
+    int rc = check_shape(who, count, rows, cols);
+    if (rc) return rc;
+    double q[3 * kMostSteps];
+    if ((rc = check_steps(who, hp->steps, hp->ns, hp->eps, q))) return rc;
+    if (hp->nesterov != 0 && hp->nesterov != 1) return bad_arg(who, "nesterov is neither 0 nor 1");
+    const float mu = (float)hp->momentum, decay = (float)(1.0 - hp->lr * hp->weight_decay), rate = (float)(hp->lr * hp->scale);
+    if (!std::isfinite(mu) || !std::isfinite(decay) || !std::isfinite(rate)) return bad_arg(who, "a hyperparameter is not finite in fp32");
+    if (count > 0 && !tensors) return bad_arg(who, "tensors is NULL");
+    const int64_t n = rows * cols;
+    const int64_t T = (int64_t)plan->numel.size();
+    try {
+        std::vector<bool> seen((size_t)T, false);
+        for (int32_t k = 0; k < count; ++k) {
+            const int32_t t = tensors[k];
+            if (t < 0 || t >= T) { set_error("%s: tensor %d is not in the plan", who, (int)t); return GSZ_ERR_INVALID_ARG; }
+            if (seen[t]) { set_error("%s: tensor %d is given twice", who, (int)t); return GSZ_ERR_INVALID_ARG; }
+            seen[t] = true;
+            if (plan->numel[t] != n) {
+                set_error("%s: tensor %d has %lld elements, not %lld x %lld", who, (int)t, (long long)plan->numel[t], (long long)rows, (long long)cols);
+                return GSZ_ERR_SIZE;
+            }
+        }
+    } catch (...) {
+        set_error("%s: out of host memory", who);
+        return GSZ_ERR_NO_MEMORY;
+    }
+    if (count == 0 || n == 0) return check_device(who);
+    if (!master || !momentum || !g || !coef || !params) return bad_arg(who, "NULL buffer");
+    if (off_by(master, 16) || off_by(momentum, 16) || off_by(g, 16) || off_by(params, 16) || off_by(coef, 4)) {
+        set_error("%s: a device pointer is not 16-byte aligned", who);
+        return GSZ_ERR_MISALIGNED;
+    }
+    const int64_t group = group_of(count);
+    const size_t need = workspace_for(group, shape_for(rows, cols, 256)).bytes;
+    if ((rc = check_workspace(who, ws, ws_bytes, need))) return rc;
+    const int64_t len = plan->flat_len;
+    const Span spans[] = {{master, len * 4}, {momentum, len * 4}, {params, len * 2}, {ws, (int64_t)need}, {g, len * 4}, {coef, 4}};
+    for (int a = 0; a < 4; ++a)
+        for (int b = a + 1; b < 6; ++b)
+            if (overlap(spans[a], spans[b])) return bad_arg(who, "buffers overlap");
+    if ((rc = check_device(who))) return rc;
+
+    const Shape s = shape_for(rows, cols, tile_for(group, rows, cols));
+    const Workspace w = workspace_for(group, s);
+    char* base = static_cast<char*>(ws);
+    double* partial = reinterpret_cast<double*>(base + w.partial);
+    double* scale = reinterpret_cast<double*>(base + w.scale);
+    const Padded p = padded(s);
+    const int64_t tiles = (p.vectors + kUpdateBlock - 1) / kUpdateBlock;
+    const MomentumArgs args{momentum, g, coef, mu, hp->nesterov};
+    for (int32_t first = 0; first < count; first += kMuonBatch) {
+        const int m = count - first < kMuonBatch ? count - first : kMuonBatch;
+        StoreUpdate last{master, params, {}, rows, cols, 1.0f / (kScaleA * kScaleX), decay, rate};
+        for (int k = 0; k < m; ++k) last.places.at[k] = plan->tensor_off[tensors[first + k]];
+        hipLaunchKernelGGL(k_momentum, dim3((unsigned)(m * s.norm_tiles)), dim3(kUpdateBlock), 0, stream, args, last.places, n, s.norm_tiles, partial);
+        if ((rc = launched(who))) return rc;
+        hipLaunchKernelGGL(k_scale, dim3((unsigned)m), dim3(kBlock), 0, stream, partial, s.norm_tiles, hp->eps, scale);
+        if ((rc = launched(who))) return rc;
+        hipLaunchKernelGGL(k_scaled_momentum, dim3((unsigned)(m * tiles)), dim3(kUpdateBlock), 0, stream, args, last.places, p, tiles, scale,
+                           reinterpret_cast<_Float16*>(base + w.x[0]));
+        if ((rc = launched(who))) return rc;
+        rc = with_tile(s.tile, [&](auto t) { return newton_schulz<decltype(t)::value>(who, m, s, w, base, hp->steps, q, last, stream); });
+        if (rc) return rc;
+    }
+    return GSZ_OK;
+}

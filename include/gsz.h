@@ -373,13 +373,78 @@ int gsz_adamw_step(float* master, float* m, float* v, const float* g, int64_t n,
                    const float* coef, const gsz_adamw_hp* hp, uint16_t* out_bf16,
                    hipStream_t stream);
 
-/* ------------------------------------------- embedding and dropout --- */
+/* ------------------------------------ orthogonalised (Muon) update --- */
 
 /* Value and id types of the calls below. */
 #define GSZ_TYPE_BF16 0
 #define GSZ_TYPE_F32 1
 #define GSZ_TYPE_I32 2
 #define GSZ_TYPE_I64 3
+
+/* Orthogonalises `count` matrices of rows x cols by Newton-Schulz steps, each matrix by
+ * itself:
+ *   X = x / (|x| + eps),  |x| the Frobenius norm (its squares summed in fp64);
+ *   steps times, with (a, b, c) = ns[3k], ns[3k + 1], ns[3k + 2] in step k:
+ *       A = X X^T,  X <- a X + (b A + c A A) X;
+ *   out = bf16(X).
+ * (A matrix with more rows than columns goes by X^T X: the same X.)  The products are summed
+ * in fp32; X, A and the polynomial are rounded to fp16 between them, scaled by 2^13, 2^12
+ * and 2^12, so the iterates' singular values must stay below 4 and the polynomial's values
+ * below 16 (the usual coefficients keep them below 1.3 and 3.5).  out is within about 0.2% of
+ * the exact result (2-norm), bf16's own rounding included.  A matrix of zeros gives zeros; one with a
+ * value that is not finite gives NaN everywhere, the others of the call unaffected.
+ *   x (device, count * rows * cols values of `type`, GSZ_TYPE_BF16 or GSZ_TYPE_F32, row by
+ *     row, one matrix after the other; any multiple of the value's size).
+ *   ns (host, 3 * steps values, each within 1e4 of 0; NULL: 3.4445, -4.7750, 2.0315 in
+ *     every step).  steps in [1, 16].  eps in [1e-30, 1e30] (1e-7 is usual).
+ *   out (device, count * rows * cols bf16): may be x itself where x is bf16; must not
+ *     overlap it otherwise.
+ *   ws (device, 16-byte aligned, >= gsz_muon_workspace_bytes): scratch apart from x and out,
+ *     per call in flight (two captured graphs that may run at once need one each).
+ * Deterministic.  GSZ_ERR_SIZE if rows or cols is over 2^17, a matrix over 2^32 elements or
+ * the workspace too small. */
+int gsz_orthogonalize(const void* x, int32_t type, int64_t count, int64_t rows, int64_t cols,
+                      int32_t steps, const double* ns, double eps, uint16_t* out, void* ws,
+                      size_t ws_bytes, hipStream_t stream);
+
+/* *out = bytes of device scratch that gsz_orthogonalize and gsz_muon_step need for `count`
+ * matrices of rows x cols, or fewer: about 4 bytes an element and 4 per element of a square
+ * of the smaller side (sides rounded up to 256), for at most 256 matrices at a time.  Needs no
+ * initialisation. */
+int gsz_muon_workspace_bytes(int64_t count, int64_t rows, int64_t cols, size_t* out);
+
+typedef struct gsz_muon_hp {
+    double lr;
+    double momentum;           /* mu */
+    double weight_decay;
+    double scale;              /* of the orthogonalised update, e.g. 0.2 sqrt(max(rows, cols)) */
+    double eps;
+    const double* ns;          /* as gsz_orthogonalize's, or NULL */
+    int32_t steps;
+    int32_t nesterov;          /* 0 or 1 */
+} gsz_muon_hp;
+
+/* The Muon update of the plan's matrices, in place in flat buffers, beside gsz_adamw_step
+ * for the other parameters (a plan of their own; gsz_clip_coef takes both plans' partials).
+ * For each listed tensor, its elements row by row in rows x cols:
+ *   gc = g*coef; m = mu*m + gc; u = nesterov ? gc + mu*m : m;
+ *   O = gsz_orthogonalize of u, not rounded to bf16;
+ *   theta = theta*(1 - lr*wd) - (lr*scale)*O;  p = bf16(theta) (round to nearest even),
+ * element by element in fp32 with one rounding per operation, the constants formed in double
+ * and rounded once.  The rest of the buffers is left as it is.
+ *   tensors (host, count forward indices): each of rows * cols elements (GSZ_ERR_SIZE
+ *     otherwise), none of them twice (GSZ_ERR_INVALID_ARG).  The plan's device tables are
+ *     not used: it need not be uploaded.
+ *   master, momentum, g (device, flat_len fp32), params (device, flat_len bf16): the plan's
+ *     flat layout (g as gsz_allreduce_mean leaves it); no two may overlap.
+ *   coef (device float, from gsz_clip_coef); ws as gsz_orthogonalize's.
+ * Ranks that share the work each list matrices of their own and gather the results. */
+int gsz_muon_step(const gsz_plan* plan, const int32_t* tensors, int32_t count, int64_t rows,
+                  int64_t cols, float* master, float* momentum, const float* g, const float* coef,
+                  const gsz_muon_hp* hp, uint16_t* params, void* ws, size_t ws_bytes,
+                  hipStream_t stream);
+
+/* ------------------------------------------- embedding and dropout --- */
 
 /* Dropout: y[e] = (add[e] or 0) + (dropped(e) ? 0 : x[e] * k), e in [0, n), in
  * fp32, rounded once to the values' type (bf16 nearest even).
@@ -458,6 +523,60 @@ int gsz_embedding_grad(const void* ids, int32_t id_type, int64_t n, const void* 
                        int64_t rows, int64_t dim, double scale, double p, const uint64_t* rng,
                        uint32_t site, void* grad, int32_t grad_type, int32_t accumulate, void* ws,
                        size_t ws_bytes, hipStream_t stream);
+
+/* --------------------------------------- relative position bias --- */
+
+/* Learned relative position bias, added to attention scores:
+ *   out[n, h, i, j] = (add[n, h, i, j] or 0) + scale * table[bucket(j - i - start_n) * heads + h]
+ * in fp32, the product and the sum rounded once each, then once to out_type.
+ *
+ * The buckets of a distance d, B = buckets: bidirectional, each direction has n = B / 2, d > 0
+ * taking the second half, and both go by |d|; else n = B and all go by max(-d, 0) (what lies
+ * ahead shares bucket 0).  With e = n / 2 (rounded down), a distance below e has a bucket of its own; one
+ * of e or more is in e + floor(log(dist / e) / log(max_distance / e) * (n - e)), n - 1 at most.
+ * The borders are whole numbers, taken from the real logarithms (a border within 2^-50 of a
+ * whole number is that number).
+ *   table (device, buckets * heads values, GSZ_TYPE_BF16 or GSZ_TYPE_F32, any multiple of the
+ *     value's size): a bucket's heads next to each other; may be read where it lies in a
+ *     bucket-flat buffer.
+ *   start_n: the place of the first query among the keys: q_start (within 2^40 of 0), or
+ *     q_starts[n] (device, batch values of start_type, GSZ_TYPE_I32 or GSZ_TYPE_I64, taken
+ *     within 2^40) where q_starts is given: new tokens of sequences of different lengths.
+ *   add, out (device, batch * heads * q_len * k_len of out_type, any multiple of the value's size):
+ *     add may be NULL, and may be out itself; out must not overlap it otherwise, nor table
+ *     or q_starts (GSZ_ERR_INVALID_ARG).  A masked score (-inf) stays masked.
+ * buckets in [2, 256], at least 2 a direction; max_distance in (e, 2^30].  GSZ_ERR_SIZE if heads
+ * is over 2^16, batch, q_len or k_len over 2^30, or there are more than 1e15 scores. */
+int gsz_relpos_bias(const void* table, int32_t table_type, int64_t buckets, int64_t heads,
+                    int64_t max_distance, int32_t bidirectional, int64_t batch, int64_t q_len,
+                    int64_t k_len, int64_t q_start, const void* q_starts, int32_t start_type,
+                    double scale, const void* add, void* out, int32_t out_type,
+                    hipStream_t stream);
+
+/* *out = bytes of device scratch gsz_relpos_bias_grad needs for exactly these sizes, per call in
+ * flight (two captured graphs that may run at once need one each).  Needs no initialisation. */
+int gsz_relpos_bias_workspace_bytes(int64_t batch, int64_t heads, int64_t q_len, int64_t k_len,
+                                    int64_t buckets, size_t* out);
+
+/* Gradient of gsz_relpos_bias with respect to the table:
+ *   grad[b * heads + h] = (accumulate ? grad[b * heads + h] : 0)
+ *       + scale * sum of dy[n, h, i, j] over the n, i, j with bucket(j - i - start_n) = b
+ * (the gradient of add is dy itself).  Sums of up to 256 values of a diagonal, and of those a
+ * tile's, are fp32, the rest fp64, in an order that depends on the sizes alone: the same call
+ * gives the same bits.  One rounding to grad_type at the end.  A masked score's dy is 0 and
+ * adds nothing.
+ *   dy (device, batch * heads * q_len * k_len of dy_type); grad (device, buckets * heads of
+ *     grad_type): both any multiple of the value's size, so grad may be the table's place in a
+ *     bf16 or fp32 bucket-flat buffer (after gsz_bucket_pack[_f32] and
+ *     gsz_bucket_accumulate[_f32], which write every tensor's place).
+ *   ws (device, 16-byte aligned, >= gsz_relpos_bias_workspace_bytes): may be NULL where none
+ *     is needed.  grad and ws must not overlap the other buffers.
+ * Errors as gsz_relpos_bias. */
+int gsz_relpos_bias_grad(const void* dy, int32_t dy_type, int64_t buckets, int64_t heads,
+                         int64_t max_distance, int32_t bidirectional, int64_t batch, int64_t q_len,
+                         int64_t k_len, int64_t q_start, const void* q_starts, int32_t start_type,
+                         double scale, void* grad, int32_t grad_type, int32_t accumulate, void* ws,
+                         size_t ws_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------ errors --- */
 

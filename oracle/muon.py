@@ -1,0 +1,66 @@
+"""Newton-Schulz orthogonalisation and the Muon update in 64 bits, and the same with the
+library's roundings of the iterates to fp16."""
+from __future__ import annotations
+
+import numpy as np
+
+NS = (3.4445, -4.7750, 2.0315)
+SCALE_X, SCALE_A = 2.0 ** 13, 2.0 ** 12      # the library holds 2^13 X, 2^12 A and 2^12 S in fp16
+
+
+def _half(v, scale):
+    return (v * scale).astype(np.float16).astype(np.float64) / scale
+
+
+def orthogonalize(x, steps=5, ns=None, eps=1e-7, rounded=False):
+    """X = x / (|x| + eps); steps times A = X X^T, X = S X with S = a I + b A + c A A, from the
+    smaller side.  rounded: X, A and S are rounded to fp16 where the library rounds them."""
+    x = np.asarray(x, dtype=np.float64)
+    if x.shape[0] > x.shape[1]:
+        return orthogonalize(x.T, steps, ns, eps, rounded).T
+    x = x / (np.sqrt((x * x).sum()) + eps)
+    for k in range(steps):
+        a, b, c = NS if ns is None else ns[k]
+        if rounded:
+            x = _half(x.astype(np.float32), SCALE_X)
+        A = x @ x.T
+        if rounded:
+            A = _half(A, SCALE_A)
+        S = a * np.eye(len(A)) + b * A + c * (A @ A)
+        if rounded:
+            S = _half(S, SCALE_A)
+        x = S @ x
+    return x
+
+
+def rounding_bound(x, steps=5, ns=None, eps=1e-7):
+    """How far (2-norm) the fp16 roundings can take the result, to first order.
+
+    f(s) = a s + b s^3 + c s^5 acts on the singular values.  A change E of X changes f(X) by at
+    most L |E|, L the largest |f'| on [0, s_max] (the divided differences of f on [-s_max, s_max]
+    are means of f').  Rounding is off by at most h = 2^-11 of a value: of X, |E| <= h |X|; of
+    A = X X^T, S changes by b E + c (A E + E A), so X by (|b| + 2 |c| s^2) s h |A|; of S, by s h |S|."""
+    x = np.asarray(x, dtype=np.float64)
+    s = np.linalg.svd(x, compute_uv=False)
+    s = s / (np.sqrt((s * s).sum()) + eps)
+    h, bound = 2.0 ** -11, 0.0
+    n2 = lambda v: float(np.sqrt((v * v).sum()))  # noqa: E731
+    for k in range(steps):
+        a, b, c = NS if ns is None else ns[k]
+        top = float(s.max())
+        t = np.linspace(0.0, top + bound, 2001)
+        slope = float(np.abs(a + 3 * b * t ** 2 + 5 * c * t ** 4).max())
+        bound = slope * (bound + h * n2(s))
+        bound += (abs(b) + 2 * abs(c) * top ** 2) * top * h * n2(s * s) + top * h * n2(a + b * s ** 2 + c * s ** 4)
+        s = np.abs(a * s + b * s ** 3 + c * s ** 5)
+        if bound > 1.0:                              # past first order: nothing is promised
+            return float("inf")
+    return bound
+
+
+def update(theta, m, g, coef, lr, mu, decay, scale, nesterov, rounded=False, **kw):
+    """(theta, m, O) after the update, in 64 bits from the fp32 arrays."""
+    gc = g.astype(np.float64) * float(coef)
+    m = mu * m.astype(np.float64) + gc
+    o = orthogonalize(gc + mu * m if nesterov else m, rounded=rounded, **kw)
+    return theta.astype(np.float64) * (1.0 - lr * decay) - lr * scale * o, m, o
