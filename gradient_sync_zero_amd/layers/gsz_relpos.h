@@ -21,7 +21,8 @@ constexpr int kRelBuckets = 256, kRelBlock = 256;
 // first[b]: the smallest distance of bucket b of one direction, non-decreasing; distances from
 // first[b] to first[b + 1] - 1 are bucket b's (none where the two are equal), the last one's all
 // from first[n - 1].
-struct RelMap { int32_t first[kRelBuckets]; int n, both; };
+// top: the largest power of two below n.
+struct RelMap { int32_t first[kRelBuckets]; int n, both, top; };
 
 // Where the first query of sequence b stands among the keys.
 struct RelStart {
@@ -36,16 +37,27 @@ struct RelStart {
     }
 };
 
-// The bucket of distance d; first: the map's borders in LDS.
-__device__ __forceinline__ int rel_bucket(const int32_t* first, int n, int both, int64_t d) {
-    const int64_t a = d > 0 ? (both ? d : 0) : -d;
-    const int32_t dist = (int32_t)(a > 0x7FFFFFFF ? 0x7FFFFFFF : a);
-    int lo = 0, hi = n - 1;                          // the last bucket that begins at or below dist
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first[mid] <= dist) lo = mid; else hi = mid - 1;
+// The buckets of N distances d, d + step ...; first: the map's borders in LDS.  The search takes the
+// same steps for all, so that their reads are under way together.
+template <int N>
+__device__ __forceinline__ void rel_buckets(const int32_t* first, const RelMap& map, int64_t d, int step, int out[N]) {
+    int32_t dist[N];
+    bool ahead[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int64_t e = d + (int64_t)j * step, a = e > 0 ? (map.both ? e : 0) : -e;
+        ahead[j] = map.both && e > 0;
+        dist[j] = (int32_t)(a > 0x7FFFFFFF ? 0x7FFFFFFF : a);
+        out[j] = 0;                                  // the last bucket that begins at or below dist
     }
-    return both && d > 0 ? lo + n : lo;
+    for (int half = map.top; half > 0; half >>= 1)
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int mid = out[j] + half;
+            if (mid < map.n && first[mid] <= dist[j]) out[j] = mid;
+        }
+#pragma unroll
+    for (int j = 0; j < N; ++j) if (ahead[j]) out[j] += map.n;
 }
 __device__ __forceinline__ void stage_map(const RelMap& m, int32_t* first) {
     for (int b = threadIdx.x; b < m.n; b += blockDim.x) first[b] = m.first[b];
@@ -53,140 +65,223 @@ __device__ __forceinline__ void stage_map(const RelMap& m, int32_t* first) {
 
 // ------------------------------------------------------------------ bias --
 
-// A tile is `rows` rows by 8 `lanes` columns of one (sequence, head); a block's work-items are
-// `lanes` across and `groups` down, each with `per` rows one below the other.
-struct BiasShape { int64_t tiles, q, k; int heads, lanes, groups, per, rows, down, across; };
+// A lane takes the values of 16 bytes of a row (8 bf16 or 4 fp32: neighbouring lanes then write
+// whole lines; 8 fp32 a lane, two stores of 16 bytes, took 37 to 58 us where this takes 31).  A
+// tile is `rows` rows by that many times `lanes` columns of one (sequence, head); a block's work-items
+// are `lanes` across and `groups` down, each with `per` rows one below the other.
+struct BiasShape { int64_t tiles, q, k, total; int buckets, heads, lanes, groups, per, rows, down, across; };
 constexpr int kBiasStrip = 8 * kRelBlock + 1024;     // columns + rows of a tile
 
-template <typename T, typename O, bool ADD>
+// 16 bytes of values, as many as a lane takes.
+template <typename O> struct Wide;
+template <> struct Wide<uint16_t> {
+    static constexpr int kWidth = 8;
+    u32x4 w;
+    template <bool NT> __device__ static Wide load(const uint16_t* p) {
+        const u32x4_at2* q = reinterpret_cast<const u32x4_at2*>(p);
+        return {NT ? __builtin_nontemporal_load(q) : *q};
+    }
+    template <bool NT> __device__ void store(uint16_t* p) const {
+        u32x4_at2* q = reinterpret_cast<u32x4_at2*>(p);
+        if (NT) __builtin_nontemporal_store(w, q); else *q = w;
+    }
+    __device__ void widen(float a[8]) const { widen8(w, a); }
+    __device__ static Wide of(const float a[8]) {
+        return {u32x4{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7])}};
+    }
+    // The first m of them, in pieces of 4, 2 and 1 (a store of each by itself made rows of 1023
+    // a half slower than rows of 1024).
+    __device__ void store_head(uint16_t* p, int m) const {
+        typedef uint32_t u32_at2 __attribute__((aligned(2)));
+        int at = 0;
+        if (m & 4) { *reinterpret_cast<u32x2_at2*>(p) = u32x2{w.x, w.y}; at = 2; }
+        if (m & 2) { *reinterpret_cast<u32_at2*>(p + 2 * at) = at ? w.z : w.x; ++at; }
+        if (m & 1) p[2 * at] = (uint16_t)(at == 0 ? w.x : at == 1 ? w.y : at == 2 ? w.z : w.w);
+    }
+};
+template <> struct Wide<float> {
+    static constexpr int kWidth = 4;
+    f32x4 w;
+    template <bool NT> __device__ static Wide load(const float* p) {
+        const f32x4_at4* q = reinterpret_cast<const f32x4_at4*>(p);
+        return {NT ? __builtin_nontemporal_load(q) : *q};
+    }
+    template <bool NT> __device__ void store(float* p) const {
+        f32x4_at4* q = reinterpret_cast<f32x4_at4*>(p);
+        if (NT) __builtin_nontemporal_store(w, q); else *q = w;
+    }
+    __device__ void widen(float a[4]) const { a[0] = w.x; a[1] = w.y; a[2] = w.z; a[3] = w.w; }
+    __device__ static Wide of(const float a[4]) { return {f32x4{a[0], a[1], a[2], a[3]}}; }
+    __device__ void store_head(float* p, int m) const {
+        typedef float f32x2_at4 __attribute__((ext_vector_type(2), aligned(4)));
+        if (m & 2) *reinterpret_cast<f32x2_at4*>(p) = f32x2{w.x, w.y};
+        if (m & 1) p[m & 2] = m & 2 ? w.z : w.x;
+    }
+};
+
+// NT: nontemporal accesses, for scores of 64 MiB and more that are added to and whose rows begin at
+// multiples of 16 bytes (4 x 32 heads of 2048 x 2048 bf16 391 us against 407, 2 x 32 of 4096 x 4096
+// 723 against 760; but 946 against 906 for 4096 x 4095, and 376 against 360 with nothing to add to).
+template <typename T, typename O, bool ADD, bool NT>
 __global__ __launch_bounds__(kRelBlock) void k_relpos_bias(const T* table, RelMap map, RelStart start, BiasShape s, float scale,
                                                            const O* add, O* out) {
+    constexpr int W = Wide<O>::kWidth;
     __shared__ int32_t first[kRelBuckets];
+    __shared__ float value[kRelBuckets];             // the head's, by bucket
     __shared__ float strip[kBiasStrip];
     stage_map(map, first);
     const int x = threadIdx.x % s.lanes, y = threadIdx.x / s.lanes;
     for (int64_t t = blockIdx.x; t < s.tiles; t += gridDim.x) {
         int64_t r = t;
-        const int64_t c0 = r % s.across * s.lanes * 8;
+        const int64_t c0 = r % s.across * s.lanes * W;
         r /= s.across;
         const int64_t i0 = r % s.down * s.rows;
         r /= s.down;
         const int head = (int)(r % s.heads);
         const int64_t d0 = c0 - (i0 + s.rows - 1) - start.of(r / s.heads);
-        __syncthreads();                             // the strip's last readers are done, the map is there
-        for (int v = threadIdx.x; v < s.rows - 1 + 8 * s.lanes; v += blockDim.x)
-            strip[v] = load1(table + (int64_t)rel_bucket(first, map.n, map.both, d0 + v) * s.heads + head) * scale;
+        for (int b = threadIdx.x; b < s.buckets; b += blockDim.x) value[b] = load1(table + (int64_t)b * s.heads + head) * scale;
+        __syncthreads();                             // the strip's last readers are done, the map and the values are there
+        const int diagonals = s.rows - 1 + W * s.lanes;
+        for (int v = threadIdx.x; v < diagonals; v += 4 * blockDim.x) {
+            int which[4];
+            rel_buckets<4>(first, map, d0 + v, blockDim.x, which);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) if (v + j * (int)blockDim.x < diagonals) strip[v + j * blockDim.x] = value[which[j]];
+        }
         __syncthreads();
-        const int64_t col = c0 + 8 * x, left = s.k - col;
+        const int64_t col = c0 + W * x;
         const int first_row = y * s.per;
-        if (y >= s.groups || left <= 0) continue;
+        if (y >= s.groups || col >= s.k) continue;
+        const int have = (int)(s.k - col < W ? s.k - col : W);
         const int64_t most = s.q - i0 - first_row;
         const int rows = (int)(most < s.per ? most : s.per);
         const int64_t at = (r * s.q + i0 + first_row) * s.k + col;
-        const int place = s.rows - 1 - first_row + 8 * x;      // of the first row's first value
-        float w[8];
+        const int place = s.rows - 1 - first_row + W * x;      // of the first row's first value
+        float w[W];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = strip[place + j];
-        const O* pa = ADD ? add + at : nullptr;
-        O* po = out + at;
-        // the window turns: after n rows its first value is w[-n mod 8]
-        int n = 0;
-        if (left >= 8) {
-            for (; n + 8 <= rows; n += 8) {
-                Raw8<O> old[8];
+        for (int j = 0; j < W; ++j) w[j] = strip[place + j];
+        // the window turns: after n rows its first value is w[-n mod W]
+        auto eight = [&](int n, int count) {
+            const int64_t p = at + n * s.k;
+            Wide<O> old[8];
+            // Values that all lie in the tensor are loaded whole, past the row's end too.
+            if (ADD && p + 7 * s.k + W <= s.total) {
 #pragma unroll
-                for (int m = 0; m < 8; ++m) if (ADD) old[m] = load8<false>(pa + (int64_t)(n + m) * s.k);
+                for (int m = 0; m < 8; ++m) old[m] = Wide<O>::template load<NT>(add + p + m * s.k);
+            } else if (ADD) {
 #pragma unroll
-                for (int m = 0; m < 8; ++m) {
-                    if (m) w[8 - m] = strip[place - n - m];
-                    else if (n) w[0] = strip[place - n];
-                    float v[8], a[8];
-                    if (ADD) widen(old[m], a);
+                for (int m = 0; m < 8; ++m)
+                    if (m < count) {
+                        const int64_t left = s.total - (p + m * s.k);
+                        float a[8] = {};
+                        if (left >= W) old[m] = Wide<O>::template load<NT>(add + p + m * s.k);
+                        else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = ADD ? a[j] + w[(8 - m + j) & 7] : w[(8 - m + j) & 7];
-                    store8<false>(po + (int64_t)(n + m) * s.k, v);
+                            for (int j = 0; j < W; ++j) if (j < left) a[j] = load1(add + p + m * s.k + j);
+                            old[m] = Wide<O>::of(a);
+                        }
+                    }
+            }
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+                if (m < count) {
+                    if (n + m) w[-m & (W - 1)] = strip[place - n - m];
+                    float v[W], a[W];
+                    if (ADD) old[m].widen(a);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) v[j] = ADD ? a[j] + w[(j - m) & (W - 1)] : w[(j - m) & (W - 1)];
+                    const Wide<O> to = Wide<O>::of(v);
+                    O* o = out + p + m * s.k;
+                    if (have == W) to.template store<NT>(o);
+                    else to.store_head(o, have);
                 }
-            }
-        }
-        for (; n < rows; ++n) {
-            float v[8], a[8];
-            if (ADD) widen(load8_part(pa + (int64_t)n * s.k, (int)(left < 8 ? left : 8)), a);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float b = strip[place - n + j];
-                v[j] = ADD ? a[j] + b : b;
-            }
-            store8_part(po + (int64_t)n * s.k, v, (int)(left < 8 ? left : 8));
-        }
+        };
+        int n = 0;
+        for (; n + 8 <= rows; n += 8) eight(n, 8);
+        if (n < rows) eight(n, rows - n);
     }
 }
 
 // -------------------------------------------------------------- gradient --
 
-// A tile is `rows` rows of one (sequence, head) and 8 `lanes` of the diagonals that cross
-// them; work-items as above.  partial[(head * buckets + b) * tiles of a head + tile]: the tile's sum
-// of bucket b.
-struct RelGradShape { int64_t tiles, per_head, q, k; int heads, buckets, lanes, groups, per, rows, down, across; };
-
-// Adds the eight values of a row from column c on that are in the row.
-template <typename T>
-__device__ __forceinline__ void add_part(const T* row, int64_t c, int64_t k, float sum[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) if (c + j >= 0 && c + j < k) sum[j] = sum[j] + load1(row + c + j);
-}
+// A work-item takes blocks of 8 rows by 8 columns, each one block further down and right than
+// the last, so that the 15 diagonals it meets stay the same and their sums stay in registers,
+// while its loads begin at multiples of 8 columns.  A tile is `rows` rows (8 `per` `groups`, the rest
+// of q at the end) of one (sequence, head) and the diagonals that its `lanes` blocks side by side
+// cross; groups lie one below the other.  partial[(head * buckets + b) * tiles of a head + tile]:
+// the tile's sum of bucket b.
+struct RelGradShape { int64_t tiles, per_head, q, k, total; int heads, buckets, lanes, groups, per, rows, down, across; };
+constexpr int kRelStrip = 8 * (kRelBlock + 32);      // 8 (lanes + 1) sums for each of up to 32 groups
 
 template <typename T>
 __global__ __launch_bounds__(kRelBlock) void k_relpos_grad(const T* dy, RelMap map, RelStart start, RelGradShape s, float* partial) {
     __shared__ int32_t first[kRelBuckets];
-    __shared__ float strip[8 * kRelBlock];
+    __shared__ float strip[kRelStrip];
     stage_map(map, first);
     const int x = threadIdx.x % s.lanes, y = threadIdx.x / s.lanes;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    const int width = 8 * s.lanes;
+    const int width = 8 * (s.lanes + 1), blocks = s.per * s.groups;
     for (int64_t t = blockIdx.x; t < s.tiles; t += gridDim.x) {
         int64_t r = t;
         const int64_t across = r % s.across;
         r /= s.across;
-        const int64_t i0 = r % s.down * s.rows;
-        const int64_t down = r % s.down;
+        const int64_t down = r % s.down, i0 = down * s.rows;
         r /= s.down;
         const int head = (int)(r % s.heads);
         const int64_t b = r / s.heads;
-        const int64_t d0 = across * width - (i0 + s.rows - 1);        // the tile's first j - i
+        // the column block of the tile's first work-item in its first row block, and the first
+        // diagonal (j - i) of the strip: that of the block's lower left corner
+        const int64_t c0 = across * s.lanes - (blocks - 1), d0 = 8 * c0 - i0 - 7;
         __syncthreads();                             // the strip's last readers are done, the map is there
-        float sum[8];
+        float sum[15];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+        for (int j = 0; j < 15; ++j) sum[j] = 0.0f;
         if (y < s.groups) {
-            const int64_t i = i0 + y * s.per, end = s.q - i0 < s.rows ? s.q - i0 : s.rows, most = end - y * s.per;
-            const int rows = (int)(most < 0 ? 0 : most < s.per ? most : s.per);
-            const T* row = dy + (r * s.q + i) * s.k;
-            int64_t c = d0 + 8 * x + i;                               // the row's column of the lane's first diagonal
-            int n = 0;
-            for (; n + 8 <= rows; n += 8, c += 8, row += 8 * s.k) {
-                if (c >= 0 && c + 15 <= s.k) {
-                    Raw8<T> v[8];
+            for (int n = 0; n < s.per; ++n) {
+                const int m = y * s.per + n;
+                const int64_t i = i0 + 8 * m, c = 8 * (c0 + x + m), rows = s.q - i;
+                if (rows <= 0 || c < 0 || c >= s.k) continue;
+                const int64_t at = (r * s.q + i) * s.k + c;
+                Raw8<T> v[8];
+                // Eight values that all lie in the tensor are loaded whole; those past the row's end
+                // are another row's and dropped below.
+                if (rows >= 8 && at + 7 * s.k + 8 <= s.total) {
 #pragma unroll
-                    for (int m = 0; m < 8; ++m) v[m] = load8<true>(row + m * s.k + c + m);
+                    for (int l = 0; l < 8; ++l) v[l] = load8<true>(dy + at + l * s.k);
+                } else {
 #pragma unroll
-                    for (int m = 0; m < 8; ++m) {
-                        float a[8];
-                        widen(v[m], a);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) sum[j] = sum[j] + a[j];
+                    for (int l = 0; l < 8; ++l) {
+                        const int64_t left = l < rows ? s.total - (at + l * s.k) : 0;
+                        v[l] = left >= 8 ? load8<true>(dy + at + l * s.k) : load8_part(dy + at + l * s.k, (int)left);
                     }
-                } else if (c + 15 > 0 && c < s.k) {
-                    for (int m = 0; m < 8; ++m) add_part(row + m * s.k, c + m, s.k, sum);
+                }
+                const int have = (int)(s.k - c < 8 ? s.k - c : 8);
+#pragma unroll
+                for (int l = 0; l < 8; ++l) {
+                    float a[8];
+                    widen(v[l], a);
+                    if (have < 8)
+#pragma unroll
+                        for (int j = 1; j < 8; ++j) a[j] = j < have ? a[j] : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[7 + j - l] = sum[7 + j - l] + a[j];
                 }
             }
-            for (; n < rows; ++n, ++c, row += s.k) add_part(row, c, s.k, sum);
+            // neighbours share seven diagonals: first the places that are a work-item's own to begin
 #pragma unroll
             for (int j = 0; j < 8; ++j) strip[y * width + 8 * x + j] = sum[j];
+            if (x == s.lanes - 1)
+#pragma unroll
+                for (int j = 8; j < 16; ++j) strip[y * width + 8 * x + j] = 0.0f;
         }
         __syncthreads();
-        // a wave a bucket: the sums of its diagonals, an interval of the tile's
+        if (y < s.groups)
+#pragma unroll
+            for (int j = 8; j < 15; ++j) strip[y * width + 8 * x + j] += sum[j];
+        __syncthreads();
+        // the sums of each bucket's diagonals, an interval of the tile's: 64 work-items a bucket, or 16
+        const int team = width * s.groups > 512 ? 64 : 16, member = threadIdx.x & (team - 1);
         const int64_t d1 = d0 - start.of(b);                          // distance of the tile's first diagonal
-        for (int k = wave; k < s.buckets; k += waves) {
+        for (int k = threadIdx.x / team; k < s.buckets; k += blockDim.x / team) {
             const bool ahead = map.both && k >= map.n;
             const int f = ahead ? k - map.n : k;
             const int64_t near = first[f], far = f + 1 < map.n ? first[f + 1] : (int64_t)1 << 62;   // distances [near, far)
@@ -198,10 +293,9 @@ __global__ __launch_bounds__(kRelBlock) void k_relpos_grad(const T* dy, RelMap m
             const int from = (int)(lo < 0 ? 0 : lo > width ? width : lo), to = (int)(hi < 0 ? 0 : hi > width ? width : hi);
             float total = 0.0f;
             for (int g = 0; g < s.groups; ++g)
-                for (int v = from + lane; v < to; v += 64) total = total + strip[g * width + v];
-#pragma unroll
-            for (int o = 32; o > 0; o >>= 1) total = total + __uint_as_float(__shfl_xor(__float_as_uint(total), o));
-            if (lane == 0) partial[((int64_t)head * s.buckets + k) * s.per_head + (b * s.down + down) * s.across + across] = total;
+                for (int v = from + member; v < to; v += team) total = total + strip[g * width + v];
+            for (int o = team / 2; o > 0; o >>= 1) total = total + __uint_as_float(__shfl_xor(__float_as_uint(total), o));
+            if (member == 0) partial[((int64_t)head * s.buckets + k) * s.per_head + (b * s.down + down) * s.across + across] = total;
         }
     }
 }

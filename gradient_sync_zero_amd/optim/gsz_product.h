@@ -193,8 +193,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(Operand L, Operand R, 
 template <int FM, int FN>
 struct Staged {
     static constexpr int kRows = 32 * FM, kCols = 32 * FN, kChunks = kCols / 8;
-    static_assert(kChunks == 8 || kChunks == 4, "swizzle");
-    __device__ static int at(int row, int chunk) { return row * kCols + (chunk ^ (row >> 1 & (kChunks - 1))) * 8; }
+    static_assert(kChunks == 8 || kChunks == 16, "swizzle");
+    __device__ static int at(int row, int chunk) { return row * kCols + (chunk ^ (kChunks == 8 ? row >> 1 & 7 : row & 15)) * 8; }
     __device__ static void put(_Float16* lds, int a, int b, int q, int lane, f16x4 v) {
         const int row = 32 * a + (lane & 31);
         *reinterpret_cast<f16x4*>(lds + at(row, 4 * b + q) + 4 * (lane >> 5)) = v;

@@ -546,7 +546,7 @@ int gsz_embedding_grad(const void* ids, int32_t id_type, int64_t n, const void* 
  *     add may be NULL, and may be out itself; out must not overlap it otherwise, nor table
  *     or q_starts (GSZ_ERR_INVALID_ARG).  A masked score (-inf) stays masked.
  * buckets in [2, 256], at least 2 a direction; max_distance in (e, 2^30].  GSZ_ERR_SIZE if heads
- * is over 2^16, batch, q_len or k_len over 2^30, or there are more than 1e15 scores. */
+ * is over 2^16, batch or q_len over 2^30, k_len over 2^20, or there are more than 1e15 scores. */
 int gsz_relpos_bias(const void* table, int32_t table_type, int64_t buckets, int64_t heads,
                     int64_t max_distance, int32_t bidirectional, int64_t batch, int64_t q_len,
                     int64_t k_len, int64_t q_start, const void* q_starts, int32_t start_type,

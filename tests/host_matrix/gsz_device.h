@@ -61,6 +61,20 @@ struct BufRes { const char* base; uint32_t bytes; };
 inline BufRes buf_res(const void* base, int64_t bytes) {
     return {static_cast<const char*>(base), bytes >= 0xFFFFFFFFll ? 0xFFFFFFFFu : (uint32_t)(bytes > 0 ? bytes : 0)};
 }
+constexpr int kCpNt = 2;
+// Dwords outside of the range read as 0, as the hardware has it.
+inline u32x4 raw_buffer_load(BufRes r, int off) {
+    u32x4 v = {0, 0, 0, 0};
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t at = (uint32_t)off + 4 * j;
+        if (at + 4 > at && (uint64_t)at + 4 <= r.bytes) { uint32_t w; std::memcpy(&w, r.base + at, 4); v[j] = w; }
+    }
+    return v;
+}
+#define __builtin_amdgcn_raw_buffer_load_b128(r, off, uniform, policy) raw_buffer_load((r), (off))
+inline f32x4 ldf4(const float* p) { f32x4 v; std::memcpy(&v, p, 16); return v; }
+inline void stf4(float* p, f32x4 v) { std::memcpy(p, &v, 16); }
+inline f32x4 add4(f32x4 a, f32x4 b) { return f32x4{a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w}; }
 inline void load_to_lds(BufRes res, _Float16* lds, int offset, int uniform) {
     const uint32_t at = (uint32_t)offset + (uint32_t)uniform;
     if (offset < 0 || uniform < 0 || (uint64_t)at + 16 > res.bytes) emu::fail("a load to LDS is out of its buffer's range");

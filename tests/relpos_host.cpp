@@ -1,5 +1,5 @@
 // The relative position bias entry points and kernels themselves, run on the CPU
-// (host_gpu/hip/hip_runtime.h) in buffers of exactly the documented sizes, against a plain
+// (host_gpu/, host_matrix/) in buffers of exactly the documented sizes, against a plain
 // reference in double.  Built with AddressSanitizer: an access outside a buffer ends the program.
 //
 //   relpos_host bias|grad batch heads q k buckets max_distance both seed
@@ -16,6 +16,7 @@ inline double __shfl_xor(double v, int mask) {
     return v;
 }
 #include "gsz_relpos.hip"
+#include "plan.cpp"
 
 #include <memory>
 #include <random>
@@ -29,14 +30,17 @@ extern "C" __bf16 __truncsfbf2(float f) {              // nearest even
     std::memcpy(&b, &h, 2);
     return b;
 }
-struct Buf {                                           // n values of a type, and nothing after them
-    std::unique_ptr<char[]> p;
+// n values of a type at place `shift` of their buffer; nothing after them but the rest of the last
+// four bytes (reads of whole 4-byte words stay on the page).
+struct Buf {
+    std::unique_ptr<char[]> raw;
+    char* p;
     int type;
-    Buf(int64_t n, int t) : p(new char[n * value_size(t) ? n * value_size(t) : 1]), type(t) {}
-    double get(int64_t i) const { return type == GSZ_TYPE_F32 ? ((float*)p.get())[i] : load1((uint16_t*)p.get() + i); }
+    Buf(int64_t n, int t, int shift = 0) : raw(new char[((n + shift) * value_size(t) + 3) / 4 * 4]), p(raw.get() + shift * value_size(t)), type(t) {}
+    double get(int64_t i) const { return type == GSZ_TYPE_F32 ? ((float*)p)[i] : load1((uint16_t*)p + i); }
     void set(int64_t i, double v) {
-        if (type == GSZ_TYPE_F32) ((float*)p.get())[i] = (float)v;
-        else { uint32_t u = __float_as_uint((float)v); ((uint16_t*)p.get())[i] = (uint16_t)(u >> 16); }
+        if (type == GSZ_TYPE_F32) ((float*)p)[i] = (float)v;
+        else { uint32_t u = __float_as_uint((float)v); ((uint16_t*)p)[i] = (uint16_t)(u >> 16); }
     }
 };
 
@@ -67,12 +71,13 @@ int main(int argc, char** argv) {
     };
     int64_t bad = 0;
     if (op == "bias") {
-        Buf table(cells, type()), out(n, type()), add(n, out.type);
+        const int shift = (int)(g() % 9);
+        Buf table(cells, type(), shift), out(n, type(), shift), add(n, out.type, 2 * shift);
         for (int64_t i = 0; i < cells; ++i) table.set(i, value());
         for (int64_t i = 0; i < n; ++i) add.set(i, value());
         const bool with = g() % 2, same = with && g() % 2;
-        const int rc = gsz_relpos_bias(table.p.get(), table.type, buckets, heads, far, both, batch, q, k, start, each ? starts.data() : nullptr,
-                                       GSZ_TYPE_I64, scale, with ? add.p.get() : nullptr, same ? add.p.get() : out.p.get(), out.type, nullptr);
+        const int rc = gsz_relpos_bias(table.p, table.type, buckets, heads, far, both, batch, q, k, start, each ? starts.data() : nullptr,
+                                       GSZ_TYPE_I64, scale, with ? add.p : nullptr, same ? add.p : out.p, out.type, nullptr);
         if (rc) { std::printf("refused %d\n", rc); return 2; }
         if (same) return 0;
         for (int64_t b = 0, at = 0; b < batch; ++b) for (int64_t h = 0; h < heads; ++h) for (int64_t i = 0; i < q; ++i) for (int64_t j = 0; j < k; ++j, ++at) {
@@ -80,7 +85,7 @@ int main(int argc, char** argv) {
             if (out.get(at) != want && ++bad < 5) std::printf("%ld %ld %ld %ld: %g, not %g\n", (long)b, (long)h, (long)i, (long)j, out.get(at), want);
         }
     } else {
-        Buf dy(n, type()), grad(cells, GSZ_TYPE_F32);
+        Buf dy(n, type(), (int)(g() % 9)), grad(cells, GSZ_TYPE_F32);
         const int acc = (int)(g() % 2);
         std::vector<double> want(cells, 0.0);
         for (int64_t i = 0; i < cells; ++i) { grad.set(i, value()); if (acc) want[i] = grad.get(i); }
@@ -93,8 +98,8 @@ int main(int argc, char** argv) {
         std::vector<char> raw(1);
         std::unique_ptr<char[]> ws(new char[bytes ? bytes : 1]);
         std::memset(ws.get(), 0xFF, bytes);
-        const int rc = gsz_relpos_bias_grad(dy.p.get(), dy.type, buckets, heads, far, both, batch, q, k, start, each ? starts.data() : nullptr,
-                                            GSZ_TYPE_I64, scale, grad.p.get(), grad.type, acc, ws.get(), bytes, nullptr);
+        const int rc = gsz_relpos_bias_grad(dy.p, dy.type, buckets, heads, far, both, batch, q, k, start, each ? starts.data() : nullptr,
+                                            GSZ_TYPE_I64, scale, grad.p, grad.type, acc, ws.get(), bytes, nullptr);
         if (rc) { std::printf("refused %d\n", rc); return 2; }
         for (int64_t i = 0; i < cells; ++i)
             if (grad.get(i) != want[i] && ++bad < 5) std::printf("bucket %ld head %ld: %g, not %g\n", (long)(i / heads), (long)(i % heads), grad.get(i), want[i]);

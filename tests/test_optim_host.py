@@ -29,7 +29,8 @@ def muon(tmp_path_factory):
 
 @pytest.fixture(scope="module")
 def relpos_host(tmp_path_factory):
-    return build(tmp_path_factory, "relpos_host", "tests/host_gpu", "include", "gradient_sync_zero_amd/layers")
+    return build(tmp_path_factory, "relpos_host", "tests/host_matrix", "tests/host_gpu", "include", "gradient_sync_zero_amd/layers",
+                 "gradient_sync_zero_amd/csrc")
 
 
 def all_pass(exe, cases):
