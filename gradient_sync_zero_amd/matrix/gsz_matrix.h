@@ -20,8 +20,12 @@ __device__ __forceinline__ void load_to_lds(BufRes res, _Float16* lds, int offse
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  : : "s"(at), "v"(offset), "s"(res), "s"(uniform) : "memory");
 }
-// This wave's loads to LDS are there.
-__device__ __forceinline__ void loads_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// All but the last PENDING of this wave's loads to LDS are there.
+template <int PENDING>
+__device__ __forceinline__ void loads_landed() {
+    static_assert(PENDING >= 0 && PENDING < 64, "a six-bit count");
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(PENDING) : "memory");
+}
 
 // ds_read_b64_tr_b16: the 16 lanes of a group give the places of 4 rows of 16 values, 4 lanes
 // a row and 4 values a lane; lane l of the group gets column l of the 4 rows.

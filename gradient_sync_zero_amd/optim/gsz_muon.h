@@ -165,27 +165,29 @@ struct StorePolynomial {
     int64_t stride, ld;
     float a, b, c;                                      // a 2^12, b, c 2^-12
     template <int FM, int FN>
-    __device__ void write(const f32x16 (&acc)[FM][FN], int64_t matrix, int64_t i, int64_t j, bool off_diagonal, int lane, _Float16* lds) const {
+    __device__ void write(const f32x16 (&acc)[FM][FN], const Place& p) const {
         using St = Staged<FM, FN>;
-        const _Float16* in = A + matrix * stride;
+        const _Float16* in = A + p.matrix * stride;
 #pragma unroll
         for (int x = 0; x < FM; ++x)
 #pragma unroll
             for (int y = 0; y < FN; ++y)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int64_t row = i + 32 * x + (lane & 31), col = j + 32 * y + 8 * q + 4 * (lane >> 5);
-                    const f16x4 old = *reinterpret_cast<const f16x4*>(in + row * ld + col);
-                    f16x4 v;
+                    const int64_t row = p.i + 32 * x + (p.lane & 31), col = p.j + 32 * y + 8 * q + 4 * (p.lane >> 5);
+                    f16x4 v = {};
+                    if (row < p.rows && col < p.cols) {
+                        const f16x4 old = *reinterpret_cast<const f16x4*>(in + row * ld + col);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[e] = (_Float16)(c * acc[x][y][4 * q + e] + b * (float)old[e] + (row == col + e ? a : 0.0f));
-                    St::put(lds, x, y, q, lane, v);
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = (_Float16)(c * acc[x][y][4 * q + e] + b * (float)old[e] + (row == col + e ? a : 0.0f));
+                    }
+                    St::put(p.lds, x, y, q, p.lane, v);
                 }
         wave_fence();
-        _Float16* m = S + matrix * stride;
-        St::rows(lds, m + i * ld + j, ld, lane);
-        if (off_diagonal) St::columns(lds, m + j * ld + i, ld, lane);
+        _Float16* m = S + p.matrix * stride;
+        St::rows(p, m, ld);
+        if (p.off_diagonal) St::columns(p, m, ld);
     }
 };
 
@@ -202,26 +204,20 @@ struct StoreResult {
     int64_t rows, cols;
     float scale;
     template <int FM, int FN>
-    __device__ void write(const f32x16 (&acc)[FM][FN], int64_t matrix, int64_t i, int64_t j, bool, int lane, _Float16*) const {
+    __device__ void write(const f32x16 (&acc)[FM][FN], const Place& p) const {
+        uint16_t* m = out + p.matrix * rows * cols;
+        by_rows(acc, p, [&](int64_t row, int64_t col, f32x4 x) {
+            if (row >= rows || col >= cols) return;
+            const float v[4] = {x.x * scale, x.y * scale, x.z * scale, x.w * scale};
+            const u32x2 w = pack4_bf16(v);
+            uint16_t* to = m + row * cols + col;
+            if (col + 4 <= cols) {
+                *reinterpret_cast<u32x2_any*>(to) = w;
+            } else {
 #pragma unroll
-        for (int x = 0; x < FM; ++x)
-#pragma unroll
-            for (int y = 0; y < FN; ++y)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int64_t row = i + 32 * x + (lane & 31), col = j + 32 * y + 8 * q + 4 * (lane >> 5);
-                    if (row >= rows || col >= cols) continue;
-                    float v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = acc[x][y][4 * q + e] * scale;
-                    const u32x2 w = pack4_bf16(v);
-                    uint16_t* p = out + (matrix * rows + row) * cols + col;
-                    if (col + 4 <= cols) {
-                        *reinterpret_cast<u32x2_any*>(p) = w;
-                    } else {
-                        for (int e = 0; e < 4; ++e) if (col + e < cols) p[e] = (uint16_t)((e & 2 ? w.y : w.x) >> 16 * (e & 1));
-                    }
-                }
+                for (int e = 0; e < 3; ++e) if (col + e < cols) to[e] = (uint16_t)((e & 2 ? w.y : w.x) >> 16 * (e & 1));
+            }
+        });
     }
 };
 
@@ -233,35 +229,29 @@ struct StoreUpdate {
     int64_t rows, cols;
     float scale, decay, rate;                            // 2^-25, 1 - lr wd, lr * the update's scale
     template <int FM, int FN>
-    __device__ void write(const f32x16 (&acc)[FM][FN], int64_t matrix, int64_t i, int64_t j, bool, int lane, _Float16*) const {
-        const int64_t at = places.at[matrix];
+    __device__ void write(const f32x16 (&acc)[FM][FN], const Place& p) const {
+        const int64_t at = places.at[p.matrix];
+        by_rows(acc, p, [&](int64_t row, int64_t col, f32x4 x) {
+            if (row >= rows || col >= cols) return;
+            float* w = master + at + row * cols + col;
+            uint16_t* to = params + at + row * cols + col;
+            if (col + 4 <= cols) {
+                const f32x4 old = *reinterpret_cast<const f32x4_any*>(w);
+                float v[4];
 #pragma unroll
-        for (int x = 0; x < FM; ++x)
+                for (int e = 0; e < 4; ++e) v[e] = old[e] * decay - rate * (x[e] * scale);
+                *reinterpret_cast<f32x4_any*>(w) = f32x4{v[0], v[1], v[2], v[3]};
+                *reinterpret_cast<u32x2_any*>(to) = pack4_bf16(v);
+            } else {
 #pragma unroll
-            for (int y = 0; y < FN; ++y)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int64_t row = i + 32 * x + (lane & 31), col = j + 32 * y + 8 * q + 4 * (lane >> 5);
-                    if (row >= rows || col >= cols) continue;
-                    float* w = master + at + row * cols + col;
-                    uint16_t* p = params + at + row * cols + col;
-                    if (col + 4 <= cols) {
-                        const f32x4 old = *reinterpret_cast<const f32x4_any*>(w);
-                        float v[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = old[e] * decay - rate * (acc[x][y][4 * q + e] * scale);
-                        *reinterpret_cast<f32x4_any*>(w) = f32x4{v[0], v[1], v[2], v[3]};
-                        *reinterpret_cast<u32x2_any*>(p) = pack4_bf16(v);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (col + e < cols) {
-                                const float v = w[e] * decay - rate * (acc[x][y][4 * q + e] * scale);
-                                w[e] = v;
-                                p[e] = (uint16_t)bf16_rne(v);
-                            }
+                for (int e = 0; e < 3; ++e)
+                    if (col + e < cols) {
+                        const float v = w[e] * decay - rate * (x[e] * scale);
+                        w[e] = v;
+                        to[e] = (uint16_t)bf16_rne(v);
                     }
-                }
+            }
+        });
     }
 };
 

@@ -73,35 +73,32 @@ int check_shape(const char* who, int64_t count, int64_t rows, int64_t cols) {
 
 int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
-// How a call of `count` matrices goes: in groups of at most kMuonBatch, with tiles of one size.
+// How a call's matrices lie in the workspace: sides padded to kStepK, groups of at most kMuonBatch.
 struct Shape {
     int64_t rows, cols, small, large;            // as given; the smaller and the larger side, padded
     int64_t padded_rows, padded_cols, norm_tiles;
-    int tile;
     bool tall;
 };
-Shape shape_for(int64_t rows, int64_t cols, int tile) {
+Shape shape_for(int64_t rows, int64_t cols) {
     Shape s{};
     s.rows = rows;
     s.cols = cols;
-    s.tile = tile;
     s.tall = rows > cols;
-    s.padded_rows = up(rows, tile);
-    s.padded_cols = up(cols, tile);
+    s.padded_rows = up(rows, kStepK);
+    s.padded_cols = up(cols, kStepK);
     s.small = s.tall ? s.padded_cols : s.padded_rows;
     s.large = s.tall ? s.padded_rows : s.padded_cols;
     s.norm_tiles = (rows * cols + kNormTile - 1) / kNormTile;
     return s;
 }
 
-int tile_for(int64_t group, int64_t rows, int64_t cols) {
-    const int64_t big = group * (up(rows, 256) / 256) * (up(cols, 256) / 256);
-    return big >= 200 ? 256 : 128;
-}
-
 int64_t group_of(int64_t count) { return count < kMuonBatch ? count : kMuonBatch; }
 
-struct Workspace { size_t partial, scale, x[2], a, s, bytes; };
+// The parts of split tiles: at most kCus of 256 KiB, or 2 kCus of 64 KiB or 16 KiB.
+constexpr int kCus = 256;
+constexpr size_t kPartialBytes = (size_t)kCus * 256 * 256 * 4;
+
+struct Workspace { size_t partial, scale, x[2], a, s, parts, bytes; };
 Workspace workspace_for(int64_t group, const Shape& s) {
     Workspace w{};
     size_t at = 0;
@@ -111,33 +108,88 @@ Workspace workspace_for(int64_t group, const Shape& s) {
     for (int k = 0; k < 2; ++k) w.x[k] = take((size_t)2 * group * s.small * s.large);
     w.a = take((size_t)2 * group * s.small * s.small);
     w.s = take((size_t)2 * group * s.small * s.small);
+    w.parts = take(kPartialBytes);
     w.bytes = at;
     return w;
 }
 
-template <int T> struct Waves;
-template <> struct Waves<256> { static constexpr int m = 2, n = 4; };
-template <> struct Waves<128> { static constexpr int m = 2, n = 2; };
+using Large = Form<256, 2, 4, 2>;                // a block a CU
+using Medium = Form<128, 2, 2, 2>;               // two
+using Small = Form<64, 2, 2, 4>;                 // two
 
-// One product over a group: C[i, j] = sum_k L[i, k] R[j, k], i < down * T, j < across * T.
-template <int T, bool TL, bool TR, class E>
-int product(const char* who, int64_t group, Operand L, Operand R, int64_t M, int64_t N, int64_t K, bool half, const E& e, hipStream_t stream) {
-    constexpr int WM = Waves<T>::m, WN = Waves<T>::n;
+// What a round of blocks takes, in us: a part for each step of 64 k, from the one where the round
+// has few blocks to the one where it has them all, and the rest.  Measured with 1 to 512 blocks of
+// 64 to 4096 k and with many rounds.
+struct Cost { int side, slots; double few, full, rest; };
+constexpr Cost kCosts[] = {{256, kCus, 1.2, 1.75, 8.0}, {128, 2 * kCus, 0.55, 1.1, 4.0}, {64, 2 * kCus, 0.27, 0.42, 2.5}};
+struct Choice { int form; int64_t whole, split; int parts; double us; };
+
+// The form and the split that take the least: the tiles of the last, partly filled round may be cut
+// along k into as many parts as fill it.  (Two products of 4096 x 4096 x 11008, symmetric: 272 tiles
+// of 256 in 493 us, the last 16 of them in 16 parts each 366 us; 20 of 64 x 64 x 10048: 44.5 us, in 20
+// parts each 17.6; twelve of 768 x 768 x 768: 25 us in tiles of 256, 13.3 in 128, 18 in 64.)
+Choice choose(int64_t group, int64_t M, int64_t N, int64_t K, bool half) {
+    Choice best{};
+    best.us = 1e30;
+    const int64_t steps = K / kStepK;
+    for (int f = 0; f < 3; ++f) {
+        const Cost& c = kCosts[f];
+        const int64_t down = (M + c.side - 1) / c.side, across = (N + c.side - 1) / c.side;
+        const int64_t tiles = group * (half ? down * (down + 1) / 2 : down * across);
+        const int64_t rounds = tiles / c.slots, tail = tiles % c.slots;
+        auto round = [&](int64_t blocks, int64_t k) { return (c.few + (c.full - c.few) * blocks / c.slots) * k + c.rest; };
+        const double before = 3.0 + rounds * round(c.slots, steps);
+        auto take = [&](int parts, double us) {
+            if (us < best.us) best = Choice{f, parts > 1 ? rounds * c.slots : tiles, parts > 1 ? tail : 0, parts, us};
+        };
+        take(1, before + (tail ? round(tail, steps) : 0.0));
+        const int64_t most = tail ? c.slots / tail : 0;
+        for (int64_t parts = 2; parts <= most && 2 * parts <= steps; ++parts) {
+            // joining: a launch, and the sums written and read back at 4 and 5 TB/s
+            const double bytes = (double)parts * tail * c.side * c.side * 4.0;
+            take((int)parts, before + round(tail * parts, (steps + parts - 1) / parts) + 5.0 + bytes * (1e6 / 4e12 + 1e6 / 5e12));
+        }
+    }
+    return best;
+}
+
+template <class F, bool TL, bool TR, class E>
+int launch(const char* who, const Choice& c, int64_t group, Operand L, Operand R, int64_t M, int64_t N, int64_t K, bool half, void* parts,
+           const E& e, hipStream_t stream) {
     Tiles t{};
-    t.down = (int)(M / T);
-    t.across = (int)(N / T);
+    t.down = (int)((M + F::kSide - 1) / F::kSide);
+    t.across = (int)((N + F::kSide - 1) / F::kSide);
     t.half = half;
     t.per = half ? t.down * (t.down + 1) / 2 : t.down * t.across;
-    t.total = group * t.per;
-    hipLaunchKernelGGL((k_product<T, T, WM, WN, TL, TR, E>), dim3((unsigned)t.total), dim3(64 * WM * WN), 0, stream, L, R, M, N, K, t, e);
+    t.whole = c.whole;
+    t.parts = c.parts;
+    t.partial = static_cast<f32x4*>(parts);
+    hipLaunchKernelGGL((k_product<F, TL, TR, E>), dim3((unsigned)(c.whole + c.split * c.parts)), dim3(64 * F::kWaves), 0, stream, L, R, M, N,
+                       K, t, e);
+    if (int rc = launched(who)) return rc;
+    if (c.split == 0) return GSZ_OK;
+    hipLaunchKernelGGL((k_join<F, E>), dim3((unsigned)(c.split * F::kWaves)), dim3(64), 0, stream, M, N, t, e);
     return launched(who);
 }
 
+// One product over a group: C[i, j] = sum_k L[i, k] R[j, k], i < M, j < N.
+template <bool TL, bool TR, class E>
+int product(const char* who, int64_t group, Operand L, Operand R, int64_t M, int64_t N, int64_t K, bool half, void* parts, const E& e,
+            hipStream_t stream, const Choice* given = nullptr) {
+    const Choice c = given ? *given : choose(group, M, N, K, half);
+    switch (c.form) {
+        case 0: return launch<Large, TL, TR>(who, c, group, L, R, M, N, K, half, parts, e, stream);
+        case 1: return launch<Medium, TL, TR>(who, c, group, L, R, M, N, K, half, parts, e, stream);
+        default: return launch<Small, TL, TR>(who, c, group, L, R, M, N, K, half, parts, e, stream);
+    }
+}
+
 // All steps of a group whose scaled matrices lie at w.x[0]; the last product goes to `last`.
-template <int T, class E>
+template <class E>
 int newton_schulz(const char* who, int64_t group, const Shape& s, const Workspace& w, char* base, int steps, const double* ns, const E& last, hipStream_t stream) {
     _Float16* A = reinterpret_cast<_Float16*>(base + w.a);
     _Float16* S = reinterpret_cast<_Float16*>(base + w.s);
+    void* parts = base + w.parts;
     const int64_t size = s.small * s.large, square = s.small * s.small;
     const Operand a{A, square, s.small}, p{S, square, s.small};
     for (int k = 0; k < steps; ++k) {
@@ -146,24 +198,19 @@ int newton_schulz(const char* who, int64_t group, const Shape& s, const Workspac
         _Float16* out = reinterpret_cast<_Float16*>(base + w.x[~k & 1]);
         const Operand x{in, size, s.padded_cols};
         const StoreHalf<true> gram{A, square, s.small, kScaleA / (kScaleX * kScaleX)};
-        int rc = s.tall ? product<T, true, true>(who, group, x, x, s.small, s.small, s.large, true, gram, stream)
-                        : product<T, false, false>(who, group, x, x, s.small, s.small, s.large, true, gram, stream);
+        int rc = s.tall ? product<true, true>(who, group, x, x, s.small, s.small, s.large, true, parts, gram, stream)
+                        : product<false, false>(who, group, x, x, s.small, s.small, s.large, true, parts, gram, stream);
         if (rc) return rc;
         const StorePolynomial poly{A, S, square, s.small, (float)(q[0] * kScaleA), (float)q[1], (float)(q[2] / kScaleA)};
-        if ((rc = product<T, false, false>(who, group, a, a, s.small, s.small, s.small, true, poly, stream))) return rc;
+        if ((rc = product<false, false>(who, group, a, a, s.small, s.small, s.small, true, parts, poly, stream))) return rc;
         auto apply = [&](const auto& e) {
-            return s.tall ? product<T, false, false>(who, group, x, p, s.large, s.small, s.small, false, e, stream)
-                          : product<T, false, true>(who, group, p, x, s.small, s.large, s.small, false, e, stream);
+            return s.tall ? product<false, false>(who, group, x, p, s.large, s.small, s.small, false, parts, e, stream)
+                          : product<false, true>(who, group, p, x, s.small, s.large, s.small, false, parts, e, stream);
         };
         rc = k + 1 < steps ? apply(StoreHalf<false>{out, size, s.padded_cols, 1.0f / kScaleA}) : apply(last);
         if (rc) return rc;
     }
     return GSZ_OK;
-}
-
-template <class F>
-int with_tile(int tile, F&& f) {
-    return tile == 256 ? f(std::integral_constant<int, 256>{}) : f(std::integral_constant<int, 128>{});
 }
 
 constexpr double kUsual[3] = {3.4445, -4.7750, 2.0315};
@@ -195,7 +242,7 @@ extern "C" int gsz_muon_workspace_bytes(int64_t count, int64_t rows, int64_t col
     const int rc = check_shape(who, count, rows, cols);
     if (rc) return rc;
     if (!out) return bad_arg(who, "NULL output");
-    *out = count && rows && cols ? workspace_for(group_of(count), shape_for(rows, cols, 256)).bytes : 0;
+    *out = count && rows && cols ? workspace_for(group_of(count), shape_for(rows, cols)).bytes : 0;
     return GSZ_OK;
 }
 
@@ -213,14 +260,14 @@ extern "C" int gsz_orthogonalize(const void* x, int32_t type, int64_t count, int
     if (!x || !out) return bad_arg(who, "NULL buffer");
     if (off_by(x, size) || off_by(out, 2)) { set_error("%s: a buffer is not aligned to its values", who); return GSZ_ERR_MISALIGNED; }
     const int64_t group = group_of(count);
-    const size_t need = workspace_for(group, shape_for(rows, cols, 256)).bytes;
+    const size_t need = workspace_for(group, shape_for(rows, cols)).bytes;
     if ((rc = check_workspace(who, ws, ws_bytes, need))) return rc;
     const Span in{x, count * n * size}, written{out, count * n * 2}, scratch{ws, (int64_t)need};
     if ((x != out || size != 2) && overlap(written, in)) return bad_arg(who, "out overlaps x");
     if (overlap(scratch, in) || overlap(scratch, written)) return bad_arg(who, "ws overlaps x or out");
     if ((rc = check_device(who))) return rc;
 
-    const Shape s = shape_for(rows, cols, tile_for(group, rows, cols));
+    const Shape s = shape_for(rows, cols);
     const Workspace w = workspace_for(group, s);
     char* base = static_cast<char*>(ws);
     double* partial = reinterpret_cast<double*>(base + w.partial);
@@ -243,7 +290,7 @@ extern "C" int gsz_orthogonalize(const void* x, int32_t type, int64_t count, int
         rc = size == 2 ? prepare(uint16_t{}) : prepare(float{});
         if (rc) return rc;
         const StoreResult last{out + first * n, rows, cols, 1.0f / (kScaleA * kScaleX)};
-        rc = with_tile(s.tile, [&](auto t) { return newton_schulz<decltype(t)::value>(who, m, s, w, base, steps, q, last, stream); });
+        rc = newton_schulz(who, m, s, w, base, steps, q, last, stream);
         if (rc) return rc;
     }
     return GSZ_OK;
@@ -287,7 +334,7 @@ extern "C" int gsz_muon_step(const gsz_plan* plan, const int32_t* tensors, int32
         return GSZ_ERR_MISALIGNED;
     }
     const int64_t group = group_of(count);
-    const size_t need = workspace_for(group, shape_for(rows, cols, 256)).bytes;
+    const size_t need = workspace_for(group, shape_for(rows, cols)).bytes;
     if ((rc = check_workspace(who, ws, ws_bytes, need))) return rc;
     const int64_t len = plan->flat_len;
     const Span spans[] = {{master, len * 4}, {momentum, len * 4}, {params, len * 2}, {ws, (int64_t)need}, {g, len * 4}, {coef, 4}};
@@ -296,7 +343,7 @@ extern "C" int gsz_muon_step(const gsz_plan* plan, const int32_t* tensors, int32
             if (overlap(spans[a], spans[b])) return bad_arg(who, "buffers overlap");
     if ((rc = check_device(who))) return rc;
 
-    const Shape s = shape_for(rows, cols, tile_for(group, rows, cols));
+    const Shape s = shape_for(rows, cols);
     const Workspace w = workspace_for(group, s);
     char* base = static_cast<char*>(ws);
     double* partial = reinterpret_cast<double*>(base + w.partial);
@@ -315,7 +362,7 @@ extern "C" int gsz_muon_step(const gsz_plan* plan, const int32_t* tensors, int32
         hipLaunchKernelGGL(k_scaled_momentum, dim3((unsigned)(m * tiles)), dim3(kUpdateBlock), 0, stream, args, last.places, p, tiles, scale,
                            reinterpret_cast<_Float16*>(base + w.x[0]));
         if ((rc = launched(who))) return rc;
-        rc = with_tile(s.tile, [&](auto t) { return newton_schulz<decltype(t)::value>(who, m, s, w, base, hp->steps, q, last, stream); });
+        rc = newton_schulz(who, m, s, w, base, hp->steps, q, last, stream);
         if (rc) return rc;
     }
     return GSZ_OK;

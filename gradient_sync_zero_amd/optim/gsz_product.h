@@ -6,7 +6,7 @@
 // or with k down its columns ("turned": element (i, k) at k * ld + i), so a product
 // with a transpose on either side needs no copy.  The next 64 of k come straight from
 // memory into LDS (16 bytes a lane, no registers) while the matrix cores work on the
-// present ones: two buffers, one barrier between them.
+// present ones: a barrier for each 64 of k.
 //
 // LDS holds a tile as it lies in memory, in 16-byte chunks whose order within a row is
 // permuted so that the lanes of a fragment's read meet every bank equally; the
@@ -16,8 +16,8 @@
 //   turned: 64 rows of BM (or BN) elements; chunk c of row k at c ^ 4 (k & 3) (rows of
 //     64: c ^ 2 (k & 2)).  ds_read_b64_tr_b16 gives lane l of 16 the column l of 4 rows of
 //     16, so two reads give a lane its eight k.
-// All sizes are multiples of the tiles: operands are padded with zeros, which the
-// products keep.
+// k is a multiple of 64: operands are padded with zeros, which the products keep.  Rows past
+// an operand's end are read as zeros (its descriptor's range ends there) and not written.
 #pragma once
 
 #include "gsz_matrix.h"
@@ -72,17 +72,17 @@ struct Tile {
 };
 
 // The tiles of one launch: `across` tiles of columns by `down` of rows a matrix, or, of a
-// symmetric result, those on and below the diagonal.
-struct Tiles { int64_t total; int per, down, across; bool half; };
+// symmetric result, those on and below the diagonal.  The first `whole` are a block's each; of
+// the others `parts` blocks take a stretch of k each and leave their sums in `partial`.
+struct Tiles { int64_t whole; int per, down, across, parts; bool half; f32x4* partial; };
 
 struct TileAt { int64_t matrix; int ti, tj; };
 
-// Blocks of one XCD take neighbouring tiles (they share its L2), columns of 8 tiles of rows.
-__device__ __forceinline__ TileAt tile_at(const Tiles& t) {
-    const int64_t b = xcd_remap(blockIdx.x, t.total);
+// Tile n: columns of 8 tiles of rows.
+__device__ __forceinline__ TileAt tile_at(const Tiles& t, int64_t index) {
     TileAt r;
-    r.matrix = b / t.per;
-    const int n = (int)(b - r.matrix * t.per);
+    r.matrix = index / t.per;
+    const int n = (int)(index - r.matrix * t.per);
     if (t.half) {
         int i = (int)((sqrtf(8.0f * n + 1.0f) - 1.0f) * 0.5f);
         while (i * (i + 1) / 2 > n) --i;
@@ -98,29 +98,45 @@ __device__ __forceinline__ TileAt tile_at(const Tiles& t) {
     return r;
 }
 
-// The product's tile, handed to the epilogue as its 32 x 32 parts: acc[a][b][r] of a lane is
-// C[i0 + 32 a + lane % 32, j0 + 32 b + 8 (r / 4) + 4 (lane / 32) + r % 4], four neighbours of
-// a row at a time.
-template <int BM, int BN, int WM, int WN, bool TL, bool TR, class Epilogue>
-__global__ __launch_bounds__(64 * WM * WN) void k_product(Operand L, Operand R, int64_t rowsL, int64_t rowsR, int64_t K,
-                                                          Tiles tiles, Epilogue epilogue) {
-    constexpr int kWaves = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
-    using TileL = Tile<BM, TL, kWaves>;
-    using TileR = Tile<BN, TR, kWaves>;
-    constexpr int kBuffer = TileL::kElems + TileR::kElems;
-    // two variables, so that the compiler sees that the loads of one do not touch the other
-    __shared__ __align__(16) _Float16 even[kBuffer], odd[kBuffer];
-    static_assert(BM * BN / 2 <= kBuffer, "the epilogue's parts fit");
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const TileAt at = tile_at(tiles);
-    const int64_t i0 = (int64_t)at.ti * BM, j0 = (int64_t)at.tj * BN;
-    const int wi = wave / WN * TM, wj = wave % WN * TN;
+// A launch's shape: tiles of SIDE x SIDE by WM x WN waves, STAGES tiles of both operands in LDS.
+template <int SIDE, int WM_, int WN_, int STAGES_>
+struct Form {
+    static constexpr int kSide = SIDE, WM = WM_, WN = WN_, kStages = STAGES_, kWaves = WM * WN;
+    static constexpr int TM = SIDE / WM, TN = SIDE / WN, FM = TM / 32, FN = TN / 32;
+    static constexpr int kBuffer = 2 * SIDE * kStepK;
+    static constexpr int kRegion = kStages * kBuffer / kWaves;      // a wave's part of LDS, fp16 values
+    // an epilogue stages the wave's tile in fp16, or 32 rows of it in fp32
+    static constexpr int kStaged = TM * TN > 64 * TN ? TM * TN : 64 * TN;
+    static_assert(kStaged <= kRegion, "the epilogue's parts fit");
+};
 
-    const _Float16* pl = L.base + at.matrix * L.stride + (TL ? i0 : i0 * L.ld);
-    const _Float16* pr = R.base + at.matrix * R.stride + (TR ? j0 : j0 * R.ld);
-    const _Float16* endL = L.base + at.matrix * L.stride + (TL ? K : rowsL) * L.ld;
-    const _Float16* endR = R.base + at.matrix * R.stride + (TR ? K : rowsR) * R.ld;
+// A wave's tile of the result: its 32 x 32 parts, acc[a][b][r] of a lane being C[i + 32 a + lane % 32,
+// j + 32 b + 8 (r / 4) + 4 (lane / 32) + r % 4], four neighbours of a row at a time.  rows, cols: C's;
+// a tile may reach past them.
+struct Place { int64_t matrix, i, j, rows, cols; bool off_diagonal; int lane; _Float16* lds; };
+
+template <class F, bool TL, bool TR, class Epilogue>
+__global__ __launch_bounds__(64 * F::kWaves) void k_product(Operand L, Operand R, int64_t rows, int64_t cols, int64_t K, Tiles tiles,
+                                                            Epilogue epilogue) {
+    constexpr int S = F::kStages, FM = F::FM, FN = F::FN, kBuffer = F::kBuffer;
+    using TileL = Tile<F::kSide, TL, F::kWaves>;
+    using TileR = Tile<F::kSide, TR, F::kWaves>;
+    __shared__ __align__(16) _Float16 lds[S * kBuffer];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // Blocks of one XCD take neighbouring tiles: they share its L2.
+    const int64_t block = blockIdx.x, rest = block - tiles.whole;
+    const int64_t index = rest < 0 ? xcd_remap(block, tiles.whole) : tiles.whole + rest / tiles.parts;
+    const int part = rest < 0 ? 0 : (int)(rest % tiles.parts), parts = rest < 0 ? 1 : tiles.parts;
+    const TileAt at = tile_at(tiles, index);
+    const int64_t i0 = (int64_t)at.ti * F::kSide, j0 = (int64_t)at.tj * F::kSide;
+    const int wi = wave / F::WN * F::TM, wj = wave % F::WN * F::TN;
+    const int all = (int)(K / kStepK), from = (int)((int64_t)all * part / parts), steps = (int)((int64_t)all * (part + 1) / parts) - from;
+
     const int64_t stepL = TL ? kStepK * L.ld : kStepK, stepR = TR ? kStepK * R.ld : kStepK;
+    const _Float16* pl = L.base + at.matrix * L.stride + (TL ? i0 : i0 * L.ld) + from * stepL;
+    const _Float16* pr = R.base + at.matrix * R.stride + (TR ? j0 : j0 * R.ld) + from * stepR;
+    const _Float16* endL = L.base + at.matrix * L.stride + (TL ? K : rows) * L.ld;
+    const _Float16* endR = R.base + at.matrix * R.stride + (TR ? K : cols) * R.ld;
     const int offL = TileL::lane_offset(wave, lane, L.ld), offR = TileR::lane_offset(wave, lane, R.ld);
 
     f32x16 acc[FM][FN];
@@ -131,11 +147,15 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(Operand L, Operand R, 
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
 
+    // Past the last step the ranges are empty: nothing is read, and the count of loads under way
+    // stays the same.
+    int loaded = 0;
     auto load = [&](_Float16* buf) {
-        TileL::load(pl, (endL - pl) * 2, L.ld, offL, wave, buf);
-        TileR::load(pr, (endR - pr) * 2, R.ld, offR, wave, buf + TileL::kElems);
+        TileL::load(pl, loaded < steps ? (endL - pl) * 2 : 0, L.ld, offL, wave, buf);
+        TileR::load(pr, loaded < steps ? (endR - pr) * 2 : 0, R.ld, offR, wave, buf + TileL::kElems);
         pl += stepL;
         pr += stepR;
+        ++loaded;
     };
     // One of the four 16-wide pieces of a tile: its fragments, and the products of those.
     f16x8 x[2][FM], y[2][FN];
@@ -153,76 +173,145 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(Operand L, Operand R, 
         interleave<FM * (TL ? 2 : 1) + FN * (TR ? 2 : 1), FM * FN>();    // the other set's reads among them
     };
     // A tile's last reads are done before the barrier that also says that the next tile is
-    // there, so the loads of the tile after that can take its buffer and the next tile's first
+    // there, so the loads of the tile S further on can take its buffer and the next tile's first
     // fragments are read while this tile's last products run.
-    const int steps = (int)(K / kStepK);
-    auto landed = [&] {
-        loads_landed();
+    constexpr int kLoads = TileL::kLoads + TileR::kLoads;
+    int now = 0;
+#pragma unroll
+    for (int n = 0; n < S; ++n) load(lds + n * kBuffer);
+    loads_landed<(S - 1) * kLoads>();
+    __syncthreads();
+    read(lds, 0, 0);
+    for (int t = 0; t < steps; ++t) {
+        _Float16* buf = lds + now;
+        now = now + kBuffer == S * kBuffer ? 0 : now + kBuffer;
+        read(buf, 1, 1);
+        multiply(0);
+        read(buf, 2, 0);
+        multiply(1);
+        read(buf, 3, 1);
+        multiply(0);
+        loads_landed<(S - 2) * kLoads>();
         __syncthreads();
-    };
-    auto tile = [&](_Float16* now, _Float16* next, int t) {
-        read(now, 1, 1);
-        multiply(0);
-        read(now, 2, 0);
+        load(buf);
+        read(lds + now, 0, 0);
         multiply(1);
-        read(now, 3, 1);
-        multiply(0);
-        landed();
-        if (t + 2 < steps) load(now);
-        if (t + 1 < steps) read(next, 0, 0);
-        multiply(1);
-    };
-    load(even);
-    landed();
-    if (steps > 1) load(odd);
-    read(even, 0, 0);
-    for (int t = 0; t < steps; t += 2) {
-        tile(even, odd, t);
-        if (t + 1 < steps) tile(odd, even, t + 1);
     }
+    loads_landed<0>();
     __syncthreads();                                                    // the buffers are the epilogue's
-    epilogue.template write<FM, FN>(acc, at.matrix, i0 + wi, j0 + wj, at.ti != at.tj, lane,
-                                    (wave < kWaves / 2 ? even : odd) + wave % (kWaves / 2) * (TM * TN));
+    if (rest < 0) {
+        epilogue.template write<FM, FN>(acc, Place{at.matrix, i0 + wi, j0 + wj, rows, cols, at.ti != at.tj, lane, lds + wave * F::kRegion});
+    } else {
+        f32x4* to = tiles.partial + (rest * F::kWaves + wave) * (FM * FN * 256) + lane;
+#pragma unroll
+        for (int a = 0; a < FM; ++a)
+#pragma unroll
+            for (int b = 0; b < FN; ++b)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    to[((a * FN + b) * 4 + q) * 64] = f32x4{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
+    }
+}
+
+// Adds up the parts of the tiles that were split, in order, and finishes them: a wave for each
+// wave's tile.
+template <class F, class Epilogue>
+__global__ __launch_bounds__(64) void k_join(int64_t rows, int64_t cols, Tiles tiles, Epilogue epilogue) {
+    constexpr int FM = F::FM, FN = F::FN;
+    __shared__ __align__(16) _Float16 lds[F::kStaged];
+    const int lane = threadIdx.x, wave = blockIdx.x % F::kWaves;
+    const int64_t split = blockIdx.x / F::kWaves;
+    const TileAt at = tile_at(tiles, tiles.whole + split);
+    f32x16 acc[FM][FN];
+    for (int part = 0; part < tiles.parts; ++part) {
+        const f32x4* in = tiles.partial + ((split * tiles.parts + part) * F::kWaves + wave) * (FM * FN * 256) + lane;
+#pragma unroll
+        for (int a = 0; a < FM; ++a)
+#pragma unroll
+            for (int b = 0; b < FN; ++b)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x4 v = in[((a * FN + b) * 4 + q) * 64];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[a][b][4 * q + e] = part ? acc[a][b][4 * q + e] + v[e] : v[e];
+                }
+    }
+    epilogue.template write<FM, FN>(acc, Place{at.matrix, (int64_t)at.ti * F::kSide + wave / F::WN * F::TM,
+                                               (int64_t)at.tj * F::kSide + wave % F::WN * F::TN, rows, cols, at.ti != at.tj, lane, lds});
 }
 
 // ------------------------------------------------------------- epilogues --
 
-// A wave's tile as fp16 through its own part of LDS, so that memory is written in whole rows:
-// four neighbours of a row go in as 8 bytes, 16-byte chunks come out.  Rows of TN elements;
-// chunk c of row r at c ^ (r >> 1 & 7).
+// The place of 16-byte chunk `chunk` of a row in a wave's part of LDS, `per` chunks a row, so that
+// lanes with a row each and lanes along a row both meet every bank equally.
+template <int PER>
+__device__ __forceinline__ int staged_chunk(int row, int chunk) {
+    static_assert(PER == 4 || PER == 8 || PER == 16, "");
+    return row * PER + (chunk ^ (PER == 16 ? row & 15 : PER == 8 ? row >> 1 & 7 : row >> 2 & 3));
+}
+
+// A wave's tile as fp16, so that memory is written in whole rows: four neighbours of a row go in
+// as 8 bytes, 16-byte chunks come out.
 template <int FM, int FN>
 struct Staged {
     static constexpr int kRows = 32 * FM, kCols = 32 * FN, kChunks = kCols / 8;
-    static_assert(kChunks == 8 || kChunks == 16, "swizzle");
-    __device__ static int at(int row, int chunk) { return row * kCols + (chunk ^ (kChunks == 8 ? row >> 1 & 7 : row & 15)) * 8; }
+    __device__ static int at(int row, int chunk) { return staged_chunk<kChunks>(row, chunk) * 8; }
     __device__ static void put(_Float16* lds, int a, int b, int q, int lane, f16x4 v) {
         const int row = 32 * a + (lane & 31);
         *reinterpret_cast<f16x4*>(lds + at(row, 4 * b + q) + 4 * (lane >> 5)) = v;
     }
-    // Writes the tile to out (its first element), rows `ld` apart.
-    __device__ static void rows(const _Float16* lds, _Float16* out, int64_t ld, int lane) {
+    // Writes the tile to its place in m, rows `ld` apart.
+    __device__ static void rows(const Place& p, _Float16* m, int64_t ld) {
         constexpr int kPer = 64 / kChunks;                          // rows an access
+        _Float16* out = m + p.i * ld + p.j;
 #pragma unroll
         for (int n = 0; n < kRows / kPer; ++n) {
-            const int row = n * kPer + lane / kChunks, c = lane % kChunks;
-            *reinterpret_cast<u32x4*>(out + row * ld + c * 8) = *reinterpret_cast<const u32x4*>(lds + at(row, c));
+            const int row = n * kPer + p.lane / kChunks, c = p.lane % kChunks;
+            if (p.i + row < p.rows && p.j + 8 * c < p.cols)
+                *reinterpret_cast<u32x4*>(out + row * ld + c * 8) = *reinterpret_cast<const u32x4*>(p.lds + at(row, c));
         }
     }
-    // Writes its transpose: row j of out takes column j.
-    __device__ static void columns(const _Float16* lds, _Float16* out, int64_t ld, int lane) {
+    // Writes its transpose to the other side of the diagonal (m is symmetric).
+    __device__ static void columns(const Place& p, _Float16* m, int64_t ld) {
+        _Float16* out = m + p.j * ld + p.i;
         // a group of 16 lanes turns 8 rows by 16 columns; the groups lie one above the other
 #pragma unroll
         for (int r0 = 0; r0 < kRows; r0 += 32)
 #pragma unroll
             for (int c0 = 0; c0 < kCols; c0 += 16) {
-                const int row = r0 + 8 * (lane >> 4) + (lane >> 2 & 3), chunk = c0 / 8 + (lane >> 1 & 1);
-                const f16x4 x = read_turned(lds + at(row, chunk) + 4 * (lane & 1));
-                const f16x4 y = read_turned(lds + at(row + 4, chunk) + 4 * (lane & 1));
-                *reinterpret_cast<f16x8*>(out + (int64_t)(c0 + (lane & 15)) * ld + r0 + 8 * (lane >> 4)) =
-                    __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+                const int row = r0 + 8 * (p.lane >> 4) + (p.lane >> 2 & 3), chunk = c0 / 8 + (p.lane >> 1 & 1);
+                const f16x4 x = read_turned(p.lds + at(row, chunk) + 4 * (p.lane & 1));
+                const f16x4 y = read_turned(p.lds + at(row + 4, chunk) + 4 * (p.lane & 1));
+                const int to = c0 + (p.lane & 15), first = r0 + 8 * (p.lane >> 4);
+                if (p.j + to < p.rows && p.i + first < p.cols)
+                    *reinterpret_cast<f16x8*>(out + to * ld + first) = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
             }
     }
 };
+
+// Hands the tile to use(row, column, four values of C) with neighbouring lanes along a row: 32 rows
+// at a time through LDS in fp32.
+template <int FM, int FN, class Use>
+__device__ __forceinline__ void by_rows(const f32x16 (&acc)[FM][FN], const Place& p, Use use) {
+    constexpr int kChunks = 8 * FN, kPer = 64 / kChunks;            // 16-byte chunks a row, rows an access
+    f32x4* lds = reinterpret_cast<f32x4*>(p.lds);
+#pragma unroll
+    for (int a = 0; a < FM; ++a) {
+        if (a) wave_fence();
+#pragma unroll
+        for (int b = 0; b < FN; ++b)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                lds[staged_chunk<kChunks>(p.lane & 31, 8 * b + 2 * q + (p.lane >> 5))] =
+                    f32x4{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
+        wave_fence();
+#pragma unroll
+        for (int n = 0; n < 32 / kPer; ++n) {
+            const int row = n * kPer + p.lane / kChunks, c = p.lane % kChunks;
+            use(p.i + 32 * a + row, p.j + 4 * c, lds[staged_chunk<kChunks>(row, c)]);
+        }
+    }
+}
 
 // out = fp16(acc * scale); a symmetric result's tile is written to both of its places.
 template <bool SYMMETRIC>
@@ -231,7 +320,7 @@ struct StoreHalf {
     int64_t stride, ld;
     float scale;
     template <int FM, int FN>
-    __device__ void write(const f32x16 (&acc)[FM][FN], int64_t matrix, int64_t i, int64_t j, bool off_diagonal, int lane, _Float16* lds) const {
+    __device__ void write(const f32x16 (&acc)[FM][FN], const Place& p) const {
         using S = Staged<FM, FN>;
 #pragma unroll
         for (int a = 0; a < FM; ++a)
@@ -239,12 +328,12 @@ struct StoreHalf {
             for (int b = 0; b < FN; ++b)
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    S::put(lds, a, b, q, lane, f16x4{(_Float16)(acc[a][b][4 * q] * scale), (_Float16)(acc[a][b][4 * q + 1] * scale),
-                                                    (_Float16)(acc[a][b][4 * q + 2] * scale), (_Float16)(acc[a][b][4 * q + 3] * scale)});
+                    S::put(p.lds, a, b, q, p.lane, f16x4{(_Float16)(acc[a][b][4 * q] * scale), (_Float16)(acc[a][b][4 * q + 1] * scale),
+                                                        (_Float16)(acc[a][b][4 * q + 2] * scale), (_Float16)(acc[a][b][4 * q + 3] * scale)});
         wave_fence();
-        _Float16* m = out + matrix * stride;
-        S::rows(lds, m + i * ld + j, ld, lane);
-        if (SYMMETRIC && off_diagonal) S::columns(lds, m + j * ld + i, ld, lane);
+        _Float16* m = out + p.matrix * stride;
+        S::rows(p, m, ld);
+        if (SYMMETRIC && p.off_diagonal) S::columns(p, m, ld);
     }
 };
 

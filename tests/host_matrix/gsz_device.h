@@ -77,12 +77,13 @@ inline void stf4(float* p, f32x4 v) { std::memcpy(p, &v, 16); }
 inline f32x4 add4(f32x4 a, f32x4 b) { return f32x4{a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w}; }
 inline void load_to_lds(BufRes res, _Float16* lds, int offset, int uniform) {
     const uint32_t at = (uint32_t)offset + (uint32_t)uniform;
-    if (offset < 0 || uniform < 0 || (uint64_t)at + 16 > res.bytes) emu::fail("a load to LDS is out of its buffer's range");
+    if (offset < 0 || uniform < 0) emu::fail("a load to LDS from before its buffer");
     _Float16* first = with_wave(lds, [](auto of) { return of(0); });
     if (first != lds) emu::fail("a load to LDS whose place is not the wave's");
-    std::memcpy(lds + 8 * lane_id(), res.base + at, 16);
+    const u32x4 v = raw_buffer_load(res, (int)at);
+    std::memcpy(lds + 8 * lane_id(), &v, 16);
 }
-inline void loads_landed() {}
+template <int PENDING> inline void loads_landed() {}
 inline f16x4 read_turned(const _Float16* lds) {
     return with_wave(lds, [](auto of) {
         const int l = lane_id(), group = l & ~15, col = l & 15;
