@@ -746,7 +746,7 @@ def _workspace(ws, dev):
 def orthogonalize(x, out, ws, steps=5, ns=None, eps=1e-7, stream=None):
     """gsz_orthogonalize: Newton-Schulz on each matrix of x, (rows, cols) or (count, rows, cols) in
     bf16 or fp32, to out, bf16 (x itself if that is bf16).  ns: (a, b, c) for each step, or None.
-    ws: a tensor of at least muon_workspace_bytes(count, rows, cols)."""
+    ws: a tensor of at least muon_workspace_bytes(count, rows, cols) (None where that is 0)."""
     if not _VALUES:
         _fill_types()
     if x is None or x.dim() not in (2, 3):
@@ -776,7 +776,8 @@ def make_muon_hp(lr, momentum=0.95, weight_decay=0.0, scale=1.0, nesterov=True, 
 def muon_step(plan, tensors, rows, cols, master, momentum, g, coef, hp, params, ws, stream=None):
     """gsz_muon_step: the Muon update of the plan's `tensors` (forward indices, each rows x cols) in
     place in the flat fp32 buffers master and momentum, g the flat gradient, params the flat bf16
-    parameters.  ws: a tensor of at least muon_workspace_bytes(len(tensors), rows, cols)."""
+    parameters.  ws: a tensor of at least muon_workspace_bytes(len(tensors), rows, cols) (None where
+    that is 0)."""
     if not _VALUES:
         _fill_types()
     lib = _lib_for(plan)

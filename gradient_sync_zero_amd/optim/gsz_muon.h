@@ -26,6 +26,7 @@ constexpr int kUpdateBlock = 256;
 constexpr int64_t kNormTile = 16 * kUpdateBlock;      // two vectors a lane
 // Matrices a launch holds: their places travel in the kernel arguments.
 constexpr int kMuonBatch = 256;
+constexpr int kMostSteps = 16;
 
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
@@ -49,53 +50,41 @@ __device__ __forceinline__ void load8_part(const T* p, int64_t m, float v[8]) {
     for (int j = 0; j < 8; ++j) v[j] = j < m ? load1(p + j) : 0.0f;
 }
 
-// Sums of squares, one a block, in fp64 and a fixed order.
-__device__ __forceinline__ void store_partial(const double s, double* out) {
-    const double total = block_sum(s);
-    if (threadIdx.x == 0) *out = total;
-}
-
+// What is orthogonalised, eight values of matrix b from its element e on, the first `left` of them
+// in the matrix and the others 0.  first() is called once for each value and makes it; again()
+// gives it once more.
 template <class T>
-__global__ __launch_bounds__(kUpdateBlock) void k_norm(const T* x, int64_t size, int64_t tiles, double* partial) {
-    const int64_t b = blockIdx.x / tiles, t = blockIdx.x % tiles;
-    double s = 0.0;
+struct Values {
+    const T* x;
+    int64_t size;
+    __device__ void first(int64_t b, int64_t e, int64_t left, float u[8]) const { load8_part(x + b * size + e, left, u); }
+    __device__ void again(int64_t b, int64_t e, int64_t left, float u[8]) const { first(b, e, left, u); }
+};
+
+// m <- mu m + g coef; u = g coef + mu m, or m.
+struct Momentum {
+    float* momentum;
+    const float* g;
+    const float* coef;
+    float mu;
+    int nesterov;
+    Places places;
+    __device__ void direction(const float m[8], const float gc[8], float u[8]) const {
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        const int64_t e = t * kNormTile + n * 8 * kUpdateBlock + 8 * threadIdx.x;
-        float u[8];
-        load8_part(x + b * size + e, size - e, u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s = s + (double)u[j] * (double)u[j];
+        for (int j = 0; j < 8; ++j) u[j] = nesterov ? gc[j] + mu * m[j] : m[j];
     }
-    store_partial(s, partial + blockIdx.x);
-}
-
-struct MomentumArgs { float* momentum; const float* g; const float* coef; float mu; int nesterov; };
-
-__device__ __forceinline__ void direction(const MomentumArgs& a, const float m[8], const float gc[8], float u[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] = a.nesterov ? gc[j] + a.mu * m[j] : m[j];
-}
-
-__global__ __launch_bounds__(kUpdateBlock) void k_momentum(MomentumArgs a, Places places, int64_t size, int64_t tiles, double* partial) {
-    const int64_t b = blockIdx.x / tiles, t = blockIdx.x % tiles, at = places.at[b];
-    const float coef = *a.coef;
-    double s = 0.0;
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        const int64_t e = t * kNormTile + n * 8 * kUpdateBlock + 8 * threadIdx.x, left = size - e;
-        float m[8], g[8], u[8];
-        load8_part(a.momentum + at + e, left, m);
-        load8_part(a.g + at + e, left, g);
+    __device__ void first(int64_t b, int64_t e, int64_t left, float u[8]) const {
+        float* p = momentum + places.at[b] + e;
+        const float c = *coef;
+        float m[8], gc[8];
+        load8_part(p, left, m);
+        load8_part(g + places.at[b] + e, left, gc);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            g[j] = g[j] * coef;
-            m[j] = a.mu * m[j] + g[j];
+            gc[j] = gc[j] * c;
+            m[j] = mu * m[j] + gc[j];
         }
-        direction(a, m, g, u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s = s + (j < left ? (double)u[j] * (double)u[j] : 0.0);
-        float* p = a.momentum + at + e;
+        direction(m, gc, u);
         if (left >= 8) {
             *reinterpret_cast<f32x4_any*>(p) = f32x4{m[0], m[1], m[2], m[3]};
             *reinterpret_cast<f32x4_any*>(p + 4) = f32x4{m[4], m[5], m[6], m[7]};
@@ -104,56 +93,67 @@ __global__ __launch_bounds__(kUpdateBlock) void k_momentum(MomentumArgs a, Place
             for (int j = 0; j < 8; ++j) if (j < left) p[j] = m[j];
         }
     }
-    store_partial(s, partial + blockIdx.x);
+    __device__ void again(int64_t b, int64_t e, int64_t left, float u[8]) const {
+        const float c = *coef;
+        float m[8], gc[8];
+        load8_part(momentum + places.at[b] + e, left, m);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) gc[j] = 0.0f;
+        if (nesterov) load8_part(g + places.at[b] + e, left, gc);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) gc[j] = gc[j] * c;
+        direction(m, gc, u);
+    }
+};
+
+// Sums of squares, one a block, in fp64 and a fixed order.
+template <class In>
+__global__ __launch_bounds__(kUpdateBlock) void k_norm(In in, int64_t size, unsigned tiles, double* partial) {
+    const unsigned b = blockIdx.x / tiles, t = blockIdx.x - b * tiles;
+    double s = 0.0;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        const int64_t e = t * kNormTile + n * 8 * kUpdateBlock + 8 * threadIdx.x, left = size - e;
+        if (left <= 0) continue;
+        float u[8];
+        in.first(b, e, left, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s = s + (j < left ? (double)u[j] * (double)u[j] : 0.0);
+    }
+    const double total = block_sum(s);
+    if (threadIdx.x == 0) partial[blockIdx.x] = total;
 }
 
-// scale[b] = 2^13 / (|U_b| + eps); NaN where U_b has a value that is not finite.
+// 2^13 / (|U| + eps) from |U|^2; NaN where U has a value that is not finite.
+__device__ __forceinline__ double norm_scale(double total, double eps) {
+    return total - total == 0.0 ? (double)kScaleX / (sqrt(total) + eps) : __builtin_nan("");
+}
 __global__ __launch_bounds__(kBlock) void k_scale(const double* partial, int64_t tiles, double eps, double* scale) {
     double s = 0.0;
     for (int64_t t = threadIdx.x; t < tiles; t += kBlock) s = s + partial[blockIdx.x * tiles + t];
     const double total = block_sum(s);
-    if (threadIdx.x == 0) scale[blockIdx.x] = total - total == 0.0 ? (double)kScaleX / (sqrt(total) + eps) : __builtin_nan("");
+    if (threadIdx.x == 0) scale[blockIdx.x] = norm_scale(total, eps);
 }
 
 // The padded matrices in fp16: eight columns a lane, zeros outside of rows x cols.
 struct Padded { int64_t rows, cols, ld, vectors; };   // ld = padded columns; vectors: ld / 8 * padded rows
-template <class Read>
-__device__ __forceinline__ void scale_tile(const Padded& p, int64_t tiles, const double* scale, _Float16* x, Read read) {
-    const int64_t b = blockIdx.x / tiles;
-    const int64_t v = (blockIdx.x % tiles) * kUpdateBlock + threadIdx.x;
+template <class In>
+__global__ __launch_bounds__(kUpdateBlock) void k_scaled(In in, Padded p, unsigned tiles, const double* scale, _Float16* x) {
+    const unsigned b = blockIdx.x / tiles;
+    const int64_t v = (int64_t)(blockIdx.x - b * tiles) * kUpdateBlock + threadIdx.x;
     if (v >= p.vectors) return;
     const int per = (int)(p.ld / 8);
-    const int64_t row = v / per;
+    const int64_t row = v < (int64_t)0xFFFFFFFFu ? (uint32_t)v / (uint32_t)per : v / per;
     const int64_t col = (v - row * per) * 8;
     float u[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) u[j] = 0.0f;
-    if (row < p.rows && col < p.cols) read(b, row * p.cols + col, p.cols - col, u);
+    if (row < p.rows && col < p.cols) in.again(b, row * p.cols + col, p.cols - col, u);
     const double s = scale[b];
     f16x8 h;
 #pragma unroll
     for (int j = 0; j < 8; ++j) h[j] = (_Float16)(float)((double)u[j] * s);
     *reinterpret_cast<f16x8*>(x + b * p.vectors * 8 + v * 8) = h;
-}
-
-template <class T>
-__global__ __launch_bounds__(kUpdateBlock) void k_scaled(const T* x, Padded p, int64_t tiles, const double* scale, _Float16* out) {
-    scale_tile(p, tiles, scale, out, [&](int64_t b, int64_t e, int64_t m, float u[8]) { load8_part(x + b * p.rows * p.cols + e, m, u); });
-}
-__global__ __launch_bounds__(kUpdateBlock) void k_scaled_momentum(MomentumArgs a, Places places, Padded p, int64_t tiles,
-                                                                  const double* scale, _Float16* out) {
-    scale_tile(p, tiles, scale, out, [&](int64_t b, int64_t e, int64_t left, float u[8]) {
-        const int64_t at = places.at[b] + e;
-        const float coef = *a.coef;
-        float m[8], g[8];
-        load8_part(a.momentum + at, left, m);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = 0.0f;
-        if (a.nesterov) load8_part(a.g + at, left, g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = g[j] * coef;
-        direction(a, m, g, u);
-    });
 }
 
 // ------------------------------------------------------------- epilogues --
@@ -198,26 +198,26 @@ __device__ __forceinline__ u32x2 pack4_bf16(const float v[4]) {
                  __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v[2], v[3]}), b2))};
 }
 
-// out = bf16(acc * scale) without the padding.
+// out = bf16(2^25 O * scale) without the padding.
 struct StoreResult {
     uint16_t* out;
     int64_t rows, cols;
     float scale;
+    // four values of a row that begin in the matrix
+    __device__ void store(int64_t matrix, int64_t row, int64_t col, f32x4 x) const {
+        const float v[4] = {x.x * scale, x.y * scale, x.z * scale, x.w * scale};
+        const u32x2 w = pack4_bf16(v);
+        uint16_t* to = out + (matrix * rows + row) * cols + col;
+        if (col + 4 <= cols) {
+            *reinterpret_cast<u32x2_any*>(to) = w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e) if (col + e < cols) to[e] = (uint16_t)((e & 2 ? w.y : w.x) >> 16 * (e & 1));
+        }
+    }
     template <int FM, int FN>
     __device__ void write(const f32x16 (&acc)[FM][FN], const Place& p) const {
-        uint16_t* m = out + p.matrix * rows * cols;
-        by_rows(acc, p, [&](int64_t row, int64_t col, f32x4 x) {
-            if (row >= rows || col >= cols) return;
-            const float v[4] = {x.x * scale, x.y * scale, x.z * scale, x.w * scale};
-            const u32x2 w = pack4_bf16(v);
-            uint16_t* to = m + row * cols + col;
-            if (col + 4 <= cols) {
-                *reinterpret_cast<u32x2_any*>(to) = w;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 3; ++e) if (col + e < cols) to[e] = (uint16_t)((e & 2 ? w.y : w.x) >> 16 * (e & 1));
-            }
-        });
+        by_rows(acc, p, [&](int64_t row, int64_t col, f32x4 x) { if (row < rows && col < cols) store(p.matrix, row, col, x); });
     }
 };
 
@@ -228,30 +228,29 @@ struct StoreUpdate {
     Places places;
     int64_t rows, cols;
     float scale, decay, rate;                            // 2^-25, 1 - lr wd, lr * the update's scale
+    __device__ void store(int64_t matrix, int64_t row, int64_t col, f32x4 x) const {
+        float* w = master + places.at[matrix] + row * cols + col;
+        uint16_t* to = params + places.at[matrix] + row * cols + col;
+        if (col + 4 <= cols) {
+            const f32x4 old = *reinterpret_cast<const f32x4_any*>(w);
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = old[e] * decay - rate * (x[e] * scale);
+            *reinterpret_cast<f32x4_any*>(w) = f32x4{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<u32x2_any*>(to) = pack4_bf16(v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (col + e < cols) {
+                    const float v = w[e] * decay - rate * (x[e] * scale);
+                    w[e] = v;
+                    to[e] = (uint16_t)bf16_rne(v);
+                }
+        }
+    }
     template <int FM, int FN>
     __device__ void write(const f32x16 (&acc)[FM][FN], const Place& p) const {
-        const int64_t at = places.at[p.matrix];
-        by_rows(acc, p, [&](int64_t row, int64_t col, f32x4 x) {
-            if (row >= rows || col >= cols) return;
-            float* w = master + at + row * cols + col;
-            uint16_t* to = params + at + row * cols + col;
-            if (col + 4 <= cols) {
-                const f32x4 old = *reinterpret_cast<const f32x4_any*>(w);
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = old[e] * decay - rate * (x[e] * scale);
-                *reinterpret_cast<f32x4_any*>(w) = f32x4{v[0], v[1], v[2], v[3]};
-                *reinterpret_cast<u32x2_any*>(to) = pack4_bf16(v);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 3; ++e)
-                    if (col + e < cols) {
-                        const float v = w[e] * decay - rate * (x[e] * scale);
-                        w[e] = v;
-                        to[e] = (uint16_t)bf16_rne(v);
-                    }
-            }
-        });
+        by_rows(acc, p, [&](int64_t row, int64_t col, f32x4 x) { if (row < rows && col < cols) store(p.matrix, row, col, x); });
     }
 };
 

@@ -1,5 +1,6 @@
 // Host half of the orthogonalising entry points of include/gsz.h: argument checks, launch
-// shapes, workspace layout.  The kernels are in gsz_muon.h and gsz_product.h.
+// shapes, workspace layout.  The kernels are in gsz_muon.h, gsz_product.h
+// and gsz_small.h.
 #pragma clang fp contract(off)
 
 #include <hip/hip_runtime.h>
@@ -10,7 +11,7 @@
 #include <type_traits>
 #include <vector>
 
-#include "gsz_muon.h"
+#include "gsz_small.h"
 
 using gsz::set_error;
 
@@ -92,19 +93,52 @@ Shape shape_for(int64_t rows, int64_t cols) {
     return s;
 }
 
+// A matrix that one block takes as a whole.
+bool fits_a_block(const Shape& s) { return s.small <= kSmallSide && s.large <= kSmallLong; }
+
 int64_t group_of(int64_t count) { return count < kMuonBatch ? count : kMuonBatch; }
 
 // The parts of split tiles: at most kCus of 256 KiB, or 2 kCus of 64 KiB or 16 KiB.
 constexpr int kCus = 256;
 constexpr size_t kPartialBytes = (size_t)kCus * 256 * 256 * 4;
 
+// Panels of matrices with a small side: about two blocks a CU, each with as many panels as that takes.
+Panels panels_for(int64_t group, const Shape& s) {
+    Panels p{};
+    const int64_t small = s.tall ? s.cols : s.rows, large = s.tall ? s.rows : s.cols;
+    p.rows = (int)s.rows;
+    p.cols = (int)s.cols;
+    p.k = (int)up(small, 32);
+    p.count = (int)((large + kPanel - 1) / kPanel);
+    p.per = (int)((group * p.count + 2 * kCus - 1) / (2 * kCus));
+    if (p.per > p.count) p.per = p.count;
+    p.parts = (p.count + p.per - 1) / p.per;
+    return p;
+}
+// The blocks of the largest number of parts that `group` matrices or fewer have.
+int64_t most_parts(int64_t group, const Shape& s) {
+    const int64_t panels = (int64_t)panels_for(1, s).count;
+    return group * panels < 3 * kCus ? group * panels : 3 * kCus;
+}
+
+Coefficients coefficients(const double* q) { return Coefficients{(float)(q[0] * kScaleA), (float)q[1], (float)(q[2] / kScaleA)}; }
+
 struct Workspace { size_t partial, scale, x[2], a, s, parts, bytes; };
 Workspace workspace_for(int64_t group, const Shape& s) {
     Workspace w{};
+    if (fits_a_block(s)) return w;
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t o = at; at += (bytes + 255) / 256 * 256; return o; };
     w.partial = take((size_t)8 * group * s.norm_tiles);
     w.scale = take((size_t)8 * group);
+    if (s.small <= kSmallSide) {
+        const Panels p = panels_for(group, s);
+        w.x[0] = take((size_t)2 * group * p.count * p.k * kPanel);
+        w.a = take((size_t)2 * group * kSmallSide * kSmallPitch);
+        w.parts = take((size_t)16 * most_parts(group, s) * kPartVectors);
+        w.bytes = at;
+        return w;
+    }
     for (int k = 0; k < 2; ++k) w.x[k] = take((size_t)2 * group * s.small * s.large);
     w.a = take((size_t)2 * group * s.small * s.small);
     w.s = take((size_t)2 * group * s.small * s.small);
@@ -201,7 +235,8 @@ int newton_schulz(const char* who, int64_t group, const Shape& s, const Workspac
         int rc = s.tall ? product<true, true>(who, group, x, x, s.small, s.small, s.large, true, parts, gram, stream)
                         : product<false, false>(who, group, x, x, s.small, s.small, s.large, true, parts, gram, stream);
         if (rc) return rc;
-        const StorePolynomial poly{A, S, square, s.small, (float)(q[0] * kScaleA), (float)q[1], (float)(q[2] / kScaleA)};
+        const Coefficients f = coefficients(q);
+        const StorePolynomial poly{A, S, square, s.small, f.a, f.b, f.c};
         if ((rc = product<false, false>(who, group, a, a, s.small, s.small, s.small, true, parts, poly, stream))) return rc;
         auto apply = [&](const auto& e) {
             return s.tall ? product<false, false>(who, group, x, p, s.large, s.small, s.small, false, parts, e, stream)
@@ -214,7 +249,6 @@ int newton_schulz(const char* who, int64_t group, const Shape& s, const Workspac
 }
 
 constexpr double kUsual[3] = {3.4445, -4.7750, 2.0315};
-constexpr int kMostSteps = 16;
 
 // The steps' coefficients: the caller's, or the usual ones for every step.
 int check_steps(const char* who, int32_t steps, const double* ns, double eps, double out[3 * kMostSteps]) {
@@ -228,12 +262,77 @@ int check_steps(const char* who, int32_t steps, const double* ns, double eps, do
 }
 
 int check_workspace(const char* who, const void* ws, size_t have, size_t need) {
+    if (need == 0) return GSZ_OK;
     if (!ws || have < need) { set_error("%s: workspace of %zu bytes required", who, need); return GSZ_ERR_SIZE; }
     if (off_by(ws, 16)) { set_error("%s: workspace is not 16-byte aligned", who); return GSZ_ERR_MISALIGNED; }
     return GSZ_OK;
 }
 
-Padded padded(const Shape& s) { return Padded{s.rows, s.cols, s.padded_cols, s.padded_rows * s.padded_cols / 8}; }
+// The norm's launches, as every form but the smallest begins.
+template <class In>
+int scale_of(const char* who, int64_t m, const Shape& s, const Workspace& w, char* base, double eps, const In& in, hipStream_t stream) {
+    double* partial = reinterpret_cast<double*>(base + w.partial);
+    hipLaunchKernelGGL((k_norm<In>), dim3((unsigned)(m * s.norm_tiles)), dim3(kUpdateBlock), 0, stream, in, s.rows * s.cols, (unsigned)s.norm_tiles, partial);
+    if (int e = launched(who)) return e;
+    hipLaunchKernelGGL(k_scale, dim3((unsigned)m), dim3(kBlock), 0, stream, partial, s.norm_tiles, eps, reinterpret_cast<double*>(base + w.scale));
+    return launched(who);
+}
+
+template <bool TALL, class In, class E>
+int panel_steps(const char* who, int64_t m, const Panels& p, const double* scale, int steps, const double* q, const In& in, const E& last,
+                hipStream_t stream) {
+    const dim3 grid((unsigned)(m * p.parts)), block(64 * kSmallWaves);
+    hipLaunchKernelGGL((k_panels<TALL, true, false, In, E>), grid, block, 0, stream, in, last, p, scale, Coefficients{});
+    if (int e = launched(who)) return e;
+    for (int k = 0; k < steps; ++k) {
+        hipLaunchKernelGGL(k_panel_sum, dim3((unsigned)(m * (kPartVectors / 64))), dim3(64), 0, stream, p);
+        if (int e = launched(who)) return e;
+        const Coefficients c = coefficients(q + 3 * k);
+        if (k + 1 < steps) hipLaunchKernelGGL((k_panels<TALL, false, false, In, E>), grid, block, 0, stream, in, last, p, scale, c);
+        else hipLaunchKernelGGL((k_panels<TALL, false, true, In, E>), grid, block, 0, stream, in, last, p, scale, c);
+        if (int e = launched(who)) return e;
+    }
+    return GSZ_OK;
+}
+
+template <class In, class E>
+int run_panels(const char* who, int64_t m, const Shape& s, const Workspace& w, char* base, int steps, const double* q, double eps, const In& in,
+               const E& last, hipStream_t stream) {
+    if (int e = scale_of(who, m, s, w, base, eps, in, stream)) return e;
+    Panels p = panels_for(m, s);
+    p.x = reinterpret_cast<_Float16*>(base + w.x[0]);
+    p.a = reinterpret_cast<_Float16*>(base + w.a);
+    p.partial = reinterpret_cast<f32x4*>(base + w.parts);
+    const double* scale = reinterpret_cast<double*>(base + w.scale);
+    return s.tall ? panel_steps<true>(who, m, p, scale, steps, q, in, last, stream) : panel_steps<false>(who, m, p, scale, steps, q, in, last, stream);
+}
+
+// Orthogonalises m matrices from `in` to `last`.
+template <class In, class E>
+int run_group(const char* who, int64_t m, const Shape& s, const Workspace& w, char* base, int steps, const double* q, double eps, const In& in,
+              const E& last, hipStream_t stream) {
+    if (fits_a_block(s)) {
+        SmallSteps z{};
+        z.count = steps;
+        for (int k = 0; k < steps; ++k) z.of[k] = coefficients(q + 3 * k);
+        auto go = [&](auto tall, auto is_long) {
+            hipLaunchKernelGGL((k_small<decltype(tall)::value, decltype(is_long)::value, In, E>), dim3((unsigned)m), dim3(64 * kSmallWaves), 0, stream,
+                               in, last, (int)s.rows, (int)s.cols, eps, z);
+        };
+        const bool is_long = s.large > kSmallPitch;
+        if (s.tall) is_long ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
+        else is_long ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
+        return launched(who);
+    }
+    if (s.small <= kSmallSide) return run_panels(who, m, s, w, base, steps, q, eps, in, last, stream);
+    if (int e = scale_of(who, m, s, w, base, eps, in, stream)) return e;
+    const double* scale = reinterpret_cast<double*>(base + w.scale);
+    const Padded p{s.rows, s.cols, s.padded_cols, s.padded_rows * s.padded_cols / 8};
+    const unsigned tiles = (unsigned)((p.vectors + kUpdateBlock - 1) / kUpdateBlock);
+    hipLaunchKernelGGL((k_scaled<In>), dim3((unsigned)(m * tiles)), dim3(kUpdateBlock), 0, stream, in, p, tiles, scale, reinterpret_cast<_Float16*>(base + w.x[0]));
+    if (int e = launched(who)) return e;
+    return newton_schulz(who, m, s, w, base, steps, q, last, stream);
+}
 
 }  // namespace
 
@@ -259,38 +358,20 @@ extern "C" int gsz_orthogonalize(const void* x, int32_t type, int64_t count, int
     if (count == 0 || n == 0) return check_device(who);
     if (!x || !out) return bad_arg(who, "NULL buffer");
     if (off_by(x, size) || off_by(out, 2)) { set_error("%s: a buffer is not aligned to its values", who); return GSZ_ERR_MISALIGNED; }
-    const int64_t group = group_of(count);
-    const size_t need = workspace_for(group, shape_for(rows, cols)).bytes;
+    const Shape s = shape_for(rows, cols);
+    const Workspace w = workspace_for(group_of(count), s);
+    const size_t need = w.bytes;
     if ((rc = check_workspace(who, ws, ws_bytes, need))) return rc;
     const Span in{x, count * n * size}, written{out, count * n * 2}, scratch{ws, (int64_t)need};
     if ((x != out || size != 2) && overlap(written, in)) return bad_arg(who, "out overlaps x");
     if (overlap(scratch, in) || overlap(scratch, written)) return bad_arg(who, "ws overlaps x or out");
     if ((rc = check_device(who))) return rc;
 
-    const Shape s = shape_for(rows, cols);
-    const Workspace w = workspace_for(group, s);
-    char* base = static_cast<char*>(ws);
-    double* partial = reinterpret_cast<double*>(base + w.partial);
-    double* scale = reinterpret_cast<double*>(base + w.scale);
-    _Float16* x0 = reinterpret_cast<_Float16*>(base + w.x[0]);
-    const Padded p = padded(s);
-    const int64_t tiles = (p.vectors + kUpdateBlock - 1) / kUpdateBlock;
     for (int64_t first = 0; first < count; first += kMuonBatch) {
         const int64_t m = count - first < kMuonBatch ? count - first : kMuonBatch;
-        auto prepare = [&](auto t) {
-            using T = decltype(t);
-            const T* from = static_cast<const T*>(x) + first * n;
-            hipLaunchKernelGGL((k_norm<T>), dim3((unsigned)(m * s.norm_tiles)), dim3(kUpdateBlock), 0, stream, from, n, s.norm_tiles, partial);
-            if (int e = launched(who)) return e;
-            hipLaunchKernelGGL(k_scale, dim3((unsigned)m), dim3(kBlock), 0, stream, partial, s.norm_tiles, eps, scale);
-            if (int e = launched(who)) return e;
-            hipLaunchKernelGGL((k_scaled<T>), dim3((unsigned)(m * tiles)), dim3(kUpdateBlock), 0, stream, from, p, tiles, scale, x0);
-            return launched(who);
-        };
-        rc = size == 2 ? prepare(uint16_t{}) : prepare(float{});
-        if (rc) return rc;
         const StoreResult last{out + first * n, rows, cols, 1.0f / (kScaleA * kScaleX)};
-        rc = newton_schulz(who, m, s, w, base, steps, q, last, stream);
+        rc = size == 2 ? run_group(who, m, s, w, static_cast<char*>(ws), steps, q, eps, Values<uint16_t>{static_cast<const uint16_t*>(x) + first * n, n}, last, stream)
+                       : run_group(who, m, s, w, static_cast<char*>(ws), steps, q, eps, Values<float>{static_cast<const float*>(x) + first * n, n}, last, stream);
         if (rc) return rc;
     }
     return GSZ_OK;
@@ -333,8 +414,9 @@ extern "C" int gsz_muon_step(const gsz_plan* plan, const int32_t* tensors, int32
         set_error("%s: a device pointer is not 16-byte aligned", who);
         return GSZ_ERR_MISALIGNED;
     }
-    const int64_t group = group_of(count);
-    const size_t need = workspace_for(group, shape_for(rows, cols)).bytes;
+    const Shape s = shape_for(rows, cols);
+    const Workspace w = workspace_for(group_of(count), s);
+    const size_t need = w.bytes;
     if ((rc = check_workspace(who, ws, ws_bytes, need))) return rc;
     const int64_t len = plan->flat_len;
     const Span spans[] = {{master, len * 4}, {momentum, len * 4}, {params, len * 2}, {ws, (int64_t)need}, {g, len * 4}, {coef, 4}};
@@ -343,27 +425,12 @@ extern "C" int gsz_muon_step(const gsz_plan* plan, const int32_t* tensors, int32
             if (overlap(spans[a], spans[b])) return bad_arg(who, "buffers overlap");
     if ((rc = check_device(who))) return rc;
 
-    const Shape s = shape_for(rows, cols);
-    const Workspace w = workspace_for(group, s);
-    char* base = static_cast<char*>(ws);
-    double* partial = reinterpret_cast<double*>(base + w.partial);
-    double* scale = reinterpret_cast<double*>(base + w.scale);
-    const Padded p = padded(s);
-    const int64_t tiles = (p.vectors + kUpdateBlock - 1) / kUpdateBlock;
-    const MomentumArgs args{momentum, g, coef, mu, hp->nesterov};
     for (int32_t first = 0; first < count; first += kMuonBatch) {
         const int m = count - first < kMuonBatch ? count - first : kMuonBatch;
+        Momentum in{momentum, g, coef, mu, hp->nesterov, {}};
         StoreUpdate last{master, params, {}, rows, cols, 1.0f / (kScaleA * kScaleX), decay, rate};
-        for (int k = 0; k < m; ++k) last.places.at[k] = plan->tensor_off[tensors[first + k]];
-        hipLaunchKernelGGL(k_momentum, dim3((unsigned)(m * s.norm_tiles)), dim3(kUpdateBlock), 0, stream, args, last.places, n, s.norm_tiles, partial);
-        if ((rc = launched(who))) return rc;
-        hipLaunchKernelGGL(k_scale, dim3((unsigned)m), dim3(kBlock), 0, stream, partial, s.norm_tiles, hp->eps, scale);
-        if ((rc = launched(who))) return rc;
-        hipLaunchKernelGGL(k_scaled_momentum, dim3((unsigned)(m * tiles)), dim3(kUpdateBlock), 0, stream, args, last.places, p, tiles, scale,
-                           reinterpret_cast<_Float16*>(base + w.x[0]));
-        if ((rc = launched(who))) return rc;
-        rc = newton_schulz(who, m, s, w, base, hp->steps, q, last, stream);
-        if (rc) return rc;
+        for (int k = 0; k < m; ++k) in.places.at[k] = last.places.at[k] = plan->tensor_off[tensors[first + k]];
+        if ((rc = run_group(who, m, s, w, static_cast<char*>(ws), hp->steps, q, hp->eps, in, last, stream))) return rc;
     }
     return GSZ_OK;
 }

@@ -400,7 +400,8 @@ int gsz_adamw_step(float* master, float* m, float* v, const float* g, int64_t n,
  *   out (device, count * rows * cols bf16): may be x itself where x is bf16; must not
  *     overlap it otherwise.
  *   ws (device, 16-byte aligned, >= gsz_muon_workspace_bytes): scratch apart from x and out,
- *     per call in flight (two captured graphs that may run at once need one each).
+ *     per call in flight (two captured graphs that may run at once need one each); may be NULL
+ *     where none is needed.
  * Deterministic.  GSZ_ERR_SIZE if rows or cols is over 2^17, a matrix over 2^32 elements or
  * the workspace too small. */
 int gsz_orthogonalize(const void* x, int32_t type, int64_t count, int64_t rows, int64_t cols,
@@ -408,9 +409,11 @@ int gsz_orthogonalize(const void* x, int32_t type, int64_t count, int64_t rows, 
                       size_t ws_bytes, hipStream_t stream);
 
 /* *out = bytes of device scratch that gsz_orthogonalize and gsz_muon_step need for `count`
- * matrices of rows x cols, or fewer: about 4 bytes an element and 4 per element of a square
- * of the smaller side (sides rounded up to 256), for at most 256 matrices at a time.  Needs no
- * initialisation. */
+ * matrices of rows x cols, or fewer: none for matrices of at most 128 by 256 (or 256 by 128); else, for
+ * at most 256 matrices at a time, about 4 bytes an element (2 where the smaller side is at most
+ * 128), 4 per element of a square of the smaller side, and up to 64 MiB for products cut along
+ * their sums.  Sides count rounded up to 64 (a long one beside a side of at most 128 to 128).
+ * Needs no initialisation. */
 int gsz_muon_workspace_bytes(int64_t count, int64_t rows, int64_t cols, size_t* out);
 
 typedef struct gsz_muon_hp {

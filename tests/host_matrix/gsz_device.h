@@ -45,6 +45,12 @@ template <class T, class F> auto with_wave(const T& mine, F f) {
     emu::sync(emu::wave());
     return r;
 }
+inline double __shfl_xor(double v, int mask) {
+    return with_wave(v, [&](auto of) { return of((emu::S.cur & 63) ^ mask); });
+}
+inline uint32_t __shfl_xor(uint32_t v, int mask) {
+    return with_wave(v, [&](auto of) { return of((emu::S.cur & 63) ^ mask); });
+}
 inline int lane_id() { return emu::S.cur & 63; }
 
 inline double block_sum(double x) {

@@ -4,17 +4,6 @@
 //
 //   relpos_host bias|grad batch heads q k buckets max_distance both seed
 //   relpos_host map buckets max_distance both      prints the buckets' borders
-#include <hip/hip_runtime.h>
-
-inline uint32_t __shfl_xor(uint32_t v, int mask) { return emu::read_lane(v, (emu::S.cur & 63) ^ mask); }
-inline double __shfl_xor(double v, int mask) {
-    uint64_t u;
-    std::memcpy(&u, &v, 8);
-    const int at = emu::S.cur ^ mask;
-    u = emu::exchange(u, [at] { if (at >= emu::S.threads || emu::S.ended[at]) emu::fail("reads a lane that has ended"); return emu::S.slot[at]; });
-    std::memcpy(&v, &u, 8);
-    return v;
-}
 #include "gsz_relpos.hip"
 #include "plan.cpp"
 

@@ -39,6 +39,8 @@ def grad(lib, dy=BUF, dt=BF16, buckets=32, heads=2, far=128, both=1, batch=1, q=
     return lib.gsz_relpos_bias_grad(dy, dt, buckets, heads, far, both, batch, q, k, start, starts, st, scale, g, gt, acc, ws, ws_bytes, None)
 
 
+BIG = dict(rows=200, cols=300)           # matrices that need a workspace
+MANY = dict(BIG, numel=(60000, 5, 60000))
 SIZES = [(dict(heads=-1), INVALID), (dict(batch=-1), INVALID), (dict(q=-1), INVALID), (dict(k=-1), INVALID), (dict(heads=1 << 17), SIZE),
          (dict(batch=(1 << 30) + 1), SIZE), (dict(q=(1 << 30) + 1), SIZE), (dict(k=(1 << 30) + 1), SIZE),
          (dict(batch=1 << 20, q=1 << 20, k=1 << 20), SIZE), (dict(buckets=1), INVALID), (dict(buckets=257), INVALID), (dict(buckets=3), INVALID),
@@ -54,8 +56,9 @@ SIZES = [(dict(heads=-1), INVALID), (dict(batch=-1), INVALID), (dict(q=-1), INVA
     (orth, dict(eps=-1.0), INVALID), (orth, dict(eps=NAN), INVALID), (orth, dict(eps=INF), INVALID), (orth, dict(steps=1, ns=[1.0, NAN, 0.0]), INVALID),
     (orth, dict(steps=1, ns=[1.0, 0.0, 1e5]), INVALID), (orth, dict(x=None), INVALID), (orth, dict(out=None), INVALID),
     (orth, dict(x=BUF + 1), MISALIGNED), (orth, dict(t=F32, x=BUF + 2), MISALIGNED), (orth, dict(out=APART + 1), MISALIGNED),
-    (orth, dict(ws=None), SIZE), (orth, dict(ws_bytes=16), SIZE), (orth, dict(ws=2 * APART + 8), MISALIGNED),
-    (orth, dict(out=BUF + 2), INVALID), (orth, dict(t=F32, out=BUF), INVALID), (orth, dict(ws=BUF), INVALID), (orth, dict(ws=APART), INVALID),
+    (orth, dict(BIG, ws=None), SIZE), (orth, dict(BIG, ws_bytes=16), SIZE), (orth, dict(BIG, ws=2 * APART + 8), MISALIGNED),
+    (orth, dict(rows=129, cols=129, ws=None), SIZE), (orth, dict(rows=257, cols=2, ws=None), SIZE),
+    (orth, dict(out=BUF + 2), INVALID), (orth, dict(t=F32, out=BUF), INVALID), (orth, dict(BIG, ws=BUF), INVALID), (orth, dict(BIG, ws=APART), INVALID),
     (muon, dict(no_plan=True), INVALID), (muon, dict(no_hp=True), INVALID), (muon, dict(no_list=True), INVALID), (muon, dict(count=-1), INVALID),
     (muon, dict(tensors=(0, 3)), INVALID), (muon, dict(tensors=(-1,)), INVALID), (muon, dict(tensors=(2, 0, 2)), INVALID),
     (muon, dict(tensors=(0, 1)), SIZE), (muon, dict(rows=8, cols=8), SIZE), (muon, dict(nesterov=False, steps=0), INVALID),
@@ -63,8 +66,8 @@ SIZES = [(dict(heads=-1), INVALID), (dict(batch=-1), INVALID), (dict(q=-1), INVA
     (muon, dict(scale=1e300), INVALID), (muon, dict(eps=0.0), INVALID),
     (muon, dict(w=None), INVALID), (muon, dict(m=None), INVALID), (muon, dict(g=None), INVALID), (muon, dict(coef=None), INVALID), (muon, dict(p=None), INVALID),
     (muon, dict(w=BUF + 8), MISALIGNED), (muon, dict(m=APART + 4), MISALIGNED), (muon, dict(g=APART + 4), MISALIGNED), (muon, dict(p=APART + 2), MISALIGNED),
-    (muon, dict(coef=BUF + 2), MISALIGNED), (muon, dict(ws=None), SIZE), (muon, dict(ws_bytes=64), SIZE), (muon, dict(ws=BUF + 8), MISALIGNED),
-    (muon, dict(m=BUF), INVALID), (muon, dict(g=BUF), INVALID), (muon, dict(g=APART), INVALID), (muon, dict(p=BUF + 64), INVALID), (muon, dict(ws=BUF), INVALID),
+    (muon, dict(coef=BUF + 2), MISALIGNED), (muon, dict(MANY, ws=None), SIZE), (muon, dict(MANY, ws_bytes=64), SIZE), (muon, dict(MANY, ws=BUF + 8), MISALIGNED),
+    (muon, dict(m=BUF), INVALID), (muon, dict(g=BUF), INVALID), (muon, dict(g=APART), INVALID), (muon, dict(p=BUF + 64), INVALID), (muon, dict(MANY, ws=BUF), INVALID),
     (muon, dict(coef=BUF + 4), INVALID),
     (bias, dict(tt=2), INVALID), (bias, dict(ot=-1), INVALID), (bias, dict(table=None), INVALID), (bias, dict(out=None), INVALID),
     (bias, dict(table=BUF + 1), MISALIGNED), (bias, dict(ot=F32, out=APART + 2), MISALIGNED), (bias, dict(add=BUF + 1), MISALIGNED),
@@ -81,13 +84,16 @@ def test_refusals(call, kw, want):
 
 
 def test_workspace_bytes():
-    for count, rows, cols in ((1, 1, 1), (3, 70, 9), (24, 2048, 2048), (300, 16, 40), (1, 28672, 8192)):
+    up = lambda v, m: (v + m - 1) // m * m  # noqa: E731
+    for count, rows, cols in ((1, 1, 257), (3, 700, 9), (24, 2048, 2048), (300, 16, 400), (1, 28672, 8192), (40, 129, 129), (256, 100, 5000)):
         b = G.muon_workspace_bytes(count, rows, cols)
-        up = lambda v: (v + 255) // 256 * 256  # noqa: E731
-        n, small = min(count, 256), min(up(rows), up(cols))
-        assert b % 256 == 0 and 4 * n * (up(rows) * up(cols) + small * small) <= b
-        assert b <= 4 * n * (up(rows) * up(cols) + small * small) + n * rows * cols // 256 + 8 * 2 * n + 2048
+        n, small, large = min(count, 256), min(rows, cols), max(rows, cols)
+        least = 2 * n * up(small, 32) * up(large, 128) if small <= 128 else 4 * n * (up(rows, 64) * up(cols, 64) + up(small, 64) ** 2)
+        assert b % 256 == 0 and least <= b
+        assert b <= least + (4 * n * 128 * 128 if small <= 128 else 0) + (64 << 20) + 8 * n * (rows * cols // 4096 + 2) + 2048
         assert b >= G.muon_workspace_bytes(count - 1, rows, cols)
+    for rows, cols in ((1, 1), (128, 256), (256, 128), (128, 128)):
+        assert G.muon_workspace_bytes(300, rows, cols) == 0
     assert G.muon_workspace_bytes(0, 5, 5) == G.muon_workspace_bytes(5, 0, 5) == 0
     assert G.relpos_bias_workspace_bytes(0, 2, 3, 4, 32) == 0
     for args in ((1, 1, 1, 1, 2), (8, 12, 1024, 1024, 32), (2, 32, 4096, 4096, 256)):
