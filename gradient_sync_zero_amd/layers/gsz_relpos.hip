@@ -74,9 +74,10 @@ int check_sizes(const char* who, int64_t batch, int64_t heads, int64_t q, int64_
 }
 
 // The buckets' borders.  Of n buckets a direction the first e = n / 2 hold one distance each; bucket
-// e + k begins at the smallest whole number at or past e (D / e)^(k / (n - e)).  That is taken in
-// 64-bit-mantissa arithmetic, and a value within 2^-50 of a whole number is that number: where
-// the power is one exactly (D / e = 16, four of eight steps), rounding does not move it up.
+// e + k begins at the smallest whole number at or past e (D / e)^(k / (n - e)).  The powers are
+// products in 64-bit mantissas, off by less than 2^-52 after 256 of them, and a value within 2^-50
+// of a whole number is that number: where the power is one exactly (D / e = 16, four of eight
+// steps), rounding does not move it up.
 int make_map(const char* who, int64_t buckets, int64_t max_distance, int32_t bidirectional, RelMap* m) {
     if (bidirectional != 0 && bidirectional != 1) return bad_arg(who, "bidirectional is neither 0 nor 1");
     const int64_t n = bidirectional ? buckets / 2 : buckets, e = n / 2;
@@ -91,9 +92,11 @@ int make_map(const char* who, int64_t buckets, int64_t max_distance, int32_t bid
     m->top = 1;
     while (2 * m->top < n) m->top *= 2;
     for (int64_t b = 0; b <= e; ++b) m->first[b] = (int32_t)b;
-    const long double ratio = std::log((long double)max_distance / e);
+    const long double ratio = std::exp(std::log((long double)max_distance / e) / (n - e));
+    long double t = e;
     for (int64_t k = 1; k < n - e; ++k) {
-        const long double t = e * std::exp(ratio * k / (n - e)), near = std::floor(t + 0.5L);
+        t *= ratio;
+        const long double near = std::floor(t + 0.5L);
         m->first[e + k] = (int32_t)(std::fabs(t - near) <= near * 0x1p-50L ? near : std::ceil(t));
     }
     return GSZ_OK;

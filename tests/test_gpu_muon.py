@@ -61,7 +61,7 @@ def check(out, x, **kw):
 
 
 SHAPES = [(1, 1), (1, 7), (5, 1), (2, 3), (17, 64), (64, 17), (63, 65), (128, 128), (129, 127), (1, 3001), (200, 500),
-          (500, 200), (300, 300), (257, 1000), (33, 2049)]
+          (500, 200), (300, 300), (257, 1000), (33, 2049), (128, 256), (256, 128), (128, 257), (257, 128), (129, 129), (96, 160), (2049, 97)]
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)
@@ -82,6 +82,15 @@ def test_many_matrices(count, rows, cols):
     # each by itself gives the same bits
     for b in some[::2]:
         assert torch.equal(run(x[b]), out[b])
+
+
+@pytest.mark.parametrize("count,rows,cols", [(1, 1100, 2300), (9, 1030, 640), (20, 900, 520), (2, 2100, 2000), (26, 64, 3001), (150, 700, 90)])
+def test_large(count, rows, cols):
+    """Every size of tiles, last rounds that are cut along the sums, and panels of several matrices."""
+    rng = np.random.default_rng(rows)
+    x = torch.from_numpy(rng.normal(0, 1, (count, rows, cols))).to(F32).cuda()
+    out = run(x)
+    check(out[[0, count - 1]], x[[0, count - 1]])
 
 
 def test_low_rank_and_wide_spectrum():

@@ -28,6 +28,12 @@ def muon(tmp_path_factory):
 
 
 @pytest.fixture(scope="module")
+def product(tmp_path_factory):
+    return build(tmp_path_factory, "product_host", "tests/host_matrix", "tests/host_gpu", "include", "gradient_sync_zero_amd/optim",
+                 "gradient_sync_zero_amd/csrc")
+
+
+@pytest.fixture(scope="module")
 def relpos_host(tmp_path_factory):
     return build(tmp_path_factory, "relpos_host", "tests/host_matrix", "tests/host_gpu", "include", "gradient_sync_zero_amd/layers",
                  "gradient_sync_zero_amd/csrc")
@@ -43,14 +49,27 @@ def all_pass(exe, cases):
     assert not bad, bad[:2]
 
 
-# count, rows, cols, type (0 bf16, 1 fp32), steps, seed
+@pytest.mark.parametrize("form", [0, 1, 2])
+def test_products(product, form):
+    """Every tile size, plain and turned operands, symmetric results, tiles that reach past the result,
+    and tiles cut along k."""
+    # parts, split, turned left, turned right, symmetric, M, N, K
+    all_pass(product, [(form, *c) for c in (
+        (1, 0, 0, 0, 0, 192, 320, 128), (1, 0, 0, 1, 0, 320, 192, 192), (1, 0, 1, 1, 0, 64, 256, 64), (1, 0, 1, 1, 1, 320, 320, 64),
+        (1, 0, 0, 0, 1, 320, 320, 128), (3, 2, 0, 1, 0, 192, 320, 448), (2, 99, 1, 1, 1, 192, 192, 320), (5, 1, 0, 0, 1, 320, 320, 320))])
+
+
+# count, rows, cols, type (0 bf16, 1 fp32), steps, seed: in one block (both orientations, and its
+# limits), in panels, as products
 @pytest.mark.parametrize("case", [(1, 1, 1, 1, 5, 1), (2, 5, 9, 0, 5, 2), (1, 9, 5, 1, 3, 3), (2, 130, 40, 1, 2, 4), (1, 33, 300, 0, 2, 5),
-                                  (1, 129, 200, 1, 2, 6), (1, 200, 129, 0, 2, 7), (3, 1, 64, 1, 5, 8), (1, 64, 1, 0, 5, 9)])
+                                  (1, 129, 200, 1, 2, 6), (1, 200, 129, 0, 2, 7), (3, 1, 64, 1, 5, 8), (1, 64, 1, 0, 5, 9),
+                                  (1, 128, 128, 1, 2, 10), (1, 128, 256, 0, 2, 11), (1, 256, 128, 1, 2, 12), (2, 97, 33, 1, 2, 13),
+                                  (1, 128, 257, 1, 2, 14), (2, 700, 100, 0, 2, 15), (3, 20, 1500, 1, 3, 16), (1, 1, 3000, 0, 5, 17), (1, 300, 1, 1, 5, 18)])
 def test_orthogonalize(muon, case):
     all_pass(muon, [case])
 
 
-@pytest.mark.parametrize("case", [(1, 7, 5, "step", 1, 1), (3, 20, 33, "step", 0, 2), (2, 140, 30, "step", 1, 3)])
+@pytest.mark.parametrize("case", [(1, 7, 5, "step", 1, 1), (3, 20, 33, "step", 0, 2), (2, 140, 30, "step", 1, 3), (2, 300, 128, "step", 1, 4), (1, 130, 200, "step", 0, 5)])
 def test_update(muon, case):
     all_pass(muon, [case])
 
