@@ -583,7 +583,7 @@ def adamw_step(master, m, v, g, coef, hp, out_bf16, stream=None):
 
 # The checks of the layer calls below cost host time that a launch of a few
 # microseconds shows, so each tensor is looked at once.
-_VALUES, _IDS, _RNG = {}, {}, {}                 # dtype -> GSZ_TYPE_*; filled on first use
+_VALUES, _IDS, _RNG, _FLOATS = {}, {}, {}, {}    # dtype -> GSZ_TYPE_*; filled on first use
 
 
 def _fill_types():
@@ -592,6 +592,7 @@ def _fill_types():
     globals()["_getRawStream"] = torch._C._cuda_getCurrentRawStream
     _IDS.update({torch.int32: 2, torch.int64: 3})
     _RNG.update({torch.int64: 3, torch.uint64: 3})
+    _FLOATS.update({torch.float32: 1})
     # last: a call of another thread that finds this filled finds all filled
     _VALUES.update({torch.bfloat16: 0, torch.uint16: 0, torch.int16: 0, torch.float32: 1})
 
@@ -783,9 +784,7 @@ def muon_step(plan, tensors, rows, cols, master, momentum, g, coef, hp, params, 
     lib = _lib_for(plan)
     count = len(tensors)
     arr = (_I32 * max(count, 1))(*tensors)
-    f32, what, n = {master.dtype: 1}, "float32", plan.flat_len
-    if _VALUES.get(master.dtype) != 1:
-        raise ValueError(f"master has dtype {master.dtype}, expected float32")
+    f32, what, n = _FLOATS, "float32", plan.flat_len
     _, wp, dev = _arg(master, "master", f32, what)
     mp = _arg(momentum, "momentum", f32, what, None, dev)[1]
     gp = _arg(g, "g", f32, what, None, dev)[1]
@@ -797,6 +796,8 @@ def muon_step(plan, tensors, rows, cols, master, momentum, g, coef, hp, params, 
         if t.numel() < least:
             raise ValueError(f"{name} has {t.numel()} elements, the call needs at least {least}")
     sp, nbytes = _workspace(ws, dev)
+    if not isinstance(hp, MuonHP):
+        raise ValueError("hp must come from make_muon_hp")
     rc = lib.gsz_muon_step(plan.handle, arr, count, rows, cols, wp, mp, gp, cp, ctypes.byref(hp), pp, sp, nbytes,
                            _layer_stream(stream, dev))
     if rc:

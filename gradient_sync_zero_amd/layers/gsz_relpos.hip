@@ -62,10 +62,9 @@ bool overlap(Span a, Span b) {
 // Sizes of a call.  All products of them fit 62 bits.
 int check_sizes(const char* who, int64_t batch, int64_t heads, int64_t q, int64_t k, int64_t buckets) {
     if (batch < 0 || heads < 0 || q < 0 || k < 0) return bad_arg(who, "negative size");
-    // k: a tile's rows lie within 2^31 bytes
-    constexpr int64_t kMost = (int64_t)1 << 30, kMostKeys = (int64_t)1 << 20;
-    if (batch > kMost || heads > 65536 || q > kMost || k > kMostKeys || (double)batch * heads * q * k > 1e15) {
-        set_error("%s: batch %lld, heads %lld, q_len %lld or k_len %lld over the limits 2^30, 2^16, 2^30, 2^20 or 1e15 scores", who,
+    constexpr int64_t kMost = (int64_t)1 << 30;
+    if (batch > kMost || heads > 65536 || q > kMost || k > kMost || (double)batch * heads * q * k > 1e15) {
+        set_error("%s: batch %lld, heads %lld, q_len %lld or k_len %lld over the limits 2^30, 2^16, 2^30, 2^30 or 1e15 scores", who,
                   (long long)batch, (long long)heads, (long long)q, (long long)k);
         return GSZ_ERR_SIZE;
     }

@@ -64,8 +64,8 @@ constexpr int64_t kMostSide = (int64_t)1 << 17, kMostElements = (int64_t)1 << 32
 
 int check_shape(const char* who, int64_t count, int64_t rows, int64_t cols) {
     if (count < 0 || rows < 0 || cols < 0) return bad_arg(who, "negative size");
-    if (rows > kMostSide || cols > kMostSide || rows * cols > kMostElements || count > (int64_t)1 << 31) {
-        set_error("%s: count %lld, rows %lld or cols %lld over the limits 2^31, 2^17, 2^17 or 2^32 elements a matrix", who,
+    if (rows > kMostSide || cols > kMostSide || rows * cols > kMostElements || count > (int64_t)1 << 31 || (double)count * rows * cols > 1e15) {
+        set_error("%s: count %lld, rows %lld or cols %lld over the limits 2^31, 2^17, 2^17, 2^32 elements a matrix or 1e15 in all", who,
                   (long long)count, (long long)rows, (long long)cols);
         return GSZ_ERR_SIZE;
     }
@@ -74,7 +74,7 @@ int check_shape(const char* who, int64_t count, int64_t rows, int64_t cols) {
 
 int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
-// How a call's matrices lie in the workspace: sides padded to kStepK, groups of at most kMuonBatch.
+// How a call's matrices lie in the workspace: sides padded to kStepK.
 struct Shape {
     int64_t rows, cols, small, large;            // as given; the smaller and the larger side, padded
     int64_t padded_rows, padded_cols, norm_tiles;
@@ -96,7 +96,14 @@ Shape shape_for(int64_t rows, int64_t cols) {
 // A matrix that one block takes as a whole.
 bool fits_a_block(const Shape& s) { return s.small <= kSmallSide && s.large <= kSmallLong; }
 
-int64_t group_of(int64_t count) { return count < kMuonBatch ? count : kMuonBatch; }
+// Matrices at a time: their places travel in the kernel arguments, and no launch over their elements,
+// eight or more a work-item, comes near 2^32 work-items.
+int64_t group_of(int64_t count, const Shape& s) {
+    constexpr int64_t kMostAtOnce = (int64_t)1 << 33;
+    int64_t most = kMostAtOnce / (s.padded_rows * s.padded_cols);
+    most = most < 1 ? 1 : most < kMuonBatch ? most : kMuonBatch;
+    return count < most ? count : most;
+}
 
 // The parts of split tiles: at most kCus of 256 KiB, or 2 kCus of 64 KiB or 16 KiB.
 constexpr int kCus = 256;
@@ -341,7 +348,8 @@ extern "C" int gsz_muon_workspace_bytes(int64_t count, int64_t rows, int64_t col
     const int rc = check_shape(who, count, rows, cols);
     if (rc) return rc;
     if (!out) return bad_arg(who, "NULL output");
-    *out = count && rows && cols ? workspace_for(group_of(count), shape_for(rows, cols)).bytes : 0;
+    const Shape s = shape_for(rows, cols);
+    *out = count && rows && cols ? workspace_for(group_of(count, s), s).bytes : 0;
     return GSZ_OK;
 }
 
@@ -359,7 +367,8 @@ extern "C" int gsz_orthogonalize(const void* x, int32_t type, int64_t count, int
     if (!x || !out) return bad_arg(who, "NULL buffer");
     if (off_by(x, size) || off_by(out, 2)) { set_error("%s: a buffer is not aligned to its values", who); return GSZ_ERR_MISALIGNED; }
     const Shape s = shape_for(rows, cols);
-    const Workspace w = workspace_for(group_of(count), s);
+    const int64_t group = group_of(count, s);
+    const Workspace w = workspace_for(group, s);
     const size_t need = w.bytes;
     if ((rc = check_workspace(who, ws, ws_bytes, need))) return rc;
     const Span in{x, count * n * size}, written{out, count * n * 2}, scratch{ws, (int64_t)need};
@@ -367,8 +376,8 @@ extern "C" int gsz_orthogonalize(const void* x, int32_t type, int64_t count, int
     if (overlap(scratch, in) || overlap(scratch, written)) return bad_arg(who, "ws overlaps x or out");
     if ((rc = check_device(who))) return rc;
 
-    for (int64_t first = 0; first < count; first += kMuonBatch) {
-        const int64_t m = count - first < kMuonBatch ? count - first : kMuonBatch;
+    for (int64_t first = 0; first < count; first += group) {
+        const int64_t m = count - first < group ? count - first : group;
         const StoreResult last{out + first * n, rows, cols, 1.0f / (kScaleA * kScaleX)};
         rc = size == 2 ? run_group(who, m, s, w, static_cast<char*>(ws), steps, q, eps, Values<uint16_t>{static_cast<const uint16_t*>(x) + first * n, n}, last, stream)
                        : run_group(who, m, s, w, static_cast<char*>(ws), steps, q, eps, Values<float>{static_cast<const float*>(x) + first * n, n}, last, stream);
@@ -415,7 +424,8 @@ extern "C" int gsz_muon_step(const gsz_plan* plan, const int32_t* tensors, int32
         return GSZ_ERR_MISALIGNED;
     }
     const Shape s = shape_for(rows, cols);
-    const Workspace w = workspace_for(group_of(count), s);
+    const int64_t group = group_of(count, s);
+    const Workspace w = workspace_for(group, s);
     const size_t need = w.bytes;
     if ((rc = check_workspace(who, ws, ws_bytes, need))) return rc;
     const int64_t len = plan->flat_len;
@@ -425,8 +435,8 @@ extern "C" int gsz_muon_step(const gsz_plan* plan, const int32_t* tensors, int32
             if (overlap(spans[a], spans[b])) return bad_arg(who, "buffers overlap");
     if ((rc = check_device(who))) return rc;
 
-    for (int32_t first = 0; first < count; first += kMuonBatch) {
-        const int m = count - first < kMuonBatch ? count - first : kMuonBatch;
+    for (int64_t first = 0; first < count; first += group) {
+        const int m = (int)(count - first < group ? count - first : group);
         Momentum in{momentum, g, coef, mu, hp->nesterov, {}};
         StoreUpdate last{master, params, {}, rows, cols, 1.0f / (kScaleA * kScaleX), decay, rate};
         for (int k = 0; k < m; ++k) in.places.at[k] = last.places.at[k] = plan->tensor_off[tensors[first + k]];

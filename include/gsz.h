@@ -14,10 +14,14 @@
  *      in all-gather layout                         (gsz_shard_adamw_step,
  *                                                    gsz_allgather_layout_write)
  *
+ * and, beside AdamW, the orthogonalised (Muon) update of whole matrices
+ * (gsz_muon_step, gsz_orthogonalize);
  * and the model's two ends of that step at its embedding: the lookup that reads
  * the table in place in the gathered parameters, its gradient written or
  * accumulated in place in a bucket, and the dropout between them
- * (gsz_embedding_lookup, gsz_embedding_grad, gsz_dropout).
+ * (gsz_embedding_lookup, gsz_embedding_grad, gsz_dropout); and its other learned
+ * table, the relative position bias of attention scores, in the same places
+ * (gsz_relpos_bias, gsz_relpos_bias_grad).
  *
  * Pages cited (title, section):
  *   "Data parallelism in depth" (infra-guide chapter 4.1)
@@ -402,15 +406,15 @@ int gsz_adamw_step(float* master, float* m, float* v, const float* g, int64_t n,
  *   ws (device, 16-byte aligned, >= gsz_muon_workspace_bytes): scratch apart from x and out,
  *     per call in flight (two captured graphs that may run at once need one each); may be NULL
  *     where none is needed.
- * Deterministic.  GSZ_ERR_SIZE if rows or cols is over 2^17, a matrix over 2^32 elements or
- * the workspace too small. */
+ * Deterministic.  GSZ_ERR_SIZE if rows or cols is over 2^17, a matrix over 2^32 elements, all of
+ * them over 1e15, count over 2^31 or the workspace too small. */
 int gsz_orthogonalize(const void* x, int32_t type, int64_t count, int64_t rows, int64_t cols,
                       int32_t steps, const double* ns, double eps, uint16_t* out, void* ws,
                       size_t ws_bytes, hipStream_t stream);
 
 /* *out = bytes of device scratch that gsz_orthogonalize and gsz_muon_step need for `count`
  * matrices of rows x cols, or fewer: none for matrices of at most 128 by 256 (or 256 by 128); else, for
- * at most 256 matrices at a time, about 4 bytes an element (2 where the smaller side is at most
+ * at most 256 matrices at a time (fewer where they hold 2^33 elements), about 4 bytes an element (2 where the smaller side is at most
  * 128), 4 per element of a square of the smaller side, and up to 64 MiB for products cut along
  * their sums.  Sides count rounded up to 64 (a long one beside a side of at most 128 to 128).
  * Needs no initialisation. */
@@ -549,7 +553,7 @@ int gsz_embedding_grad(const void* ids, int32_t id_type, int64_t n, const void* 
  *     add may be NULL, and may be out itself; out must not overlap it otherwise, nor table
  *     or q_starts (GSZ_ERR_INVALID_ARG).  A masked score (-inf) stays masked.
  * buckets in [2, 256], at least 2 a direction; max_distance in (e, 2^30].  GSZ_ERR_SIZE if heads
- * is over 2^16, batch or q_len over 2^30, k_len over 2^20, or there are more than 1e15 scores. */
+ * is over 2^16, batch, q_len or k_len over 2^30, or there are more than 1e15 scores. */
 int gsz_relpos_bias(const void* table, int32_t table_type, int64_t buckets, int64_t heads,
                     int64_t max_distance, int32_t bidirectional, int64_t batch, int64_t q_len,
                     int64_t k_len, int64_t q_start, const void* q_starts, int32_t start_type,

@@ -23,6 +23,9 @@ Modules and the step they cover:
   ledger   bytes per parameter for DDP and the ZeRO stages
   lsq      least-squares model for the gradient-mean equivalence
   step     composed shard step and the unsharded (DDP) reference
+Beside them, from the operations' own definitions: embedding (lookup, gradient, dropout),
+muon (Newton-Schulz orthogonalisation and the update built on it) and relpos (the
+relative position bias and its gradient).
 
 Every function here is pinned by a test against something other than itself
 (values printed on the pages, closed forms, invariants, library routines,

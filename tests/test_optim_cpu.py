@@ -52,7 +52,7 @@ SIZES = [(dict(heads=-1), INVALID), (dict(batch=-1), INVALID), (dict(q=-1), INVA
 @pytest.mark.parametrize("call,kw,want", [
     (orth, dict(t=2), INVALID), (orth, dict(count=-1), INVALID), (orth, dict(rows=-1), INVALID), (orth, dict(cols=-1), INVALID),
     (orth, dict(rows=(1 << 17) + 1), SIZE), (orth, dict(cols=(1 << 17) + 1), SIZE), (orth, dict(rows=1 << 17, cols=(1 << 15) + 1), SIZE),
-    (orth, dict(count=(1 << 31) + 1), SIZE), (orth, dict(steps=0), INVALID), (orth, dict(steps=17), INVALID), (orth, dict(eps=0.0), INVALID),
+    (orth, dict(count=(1 << 31) + 1), SIZE), (orth, dict(count=1 << 31, rows=1 << 10, cols=1 << 10), SIZE), (orth, dict(steps=0), INVALID), (orth, dict(steps=17), INVALID), (orth, dict(eps=0.0), INVALID),
     (orth, dict(eps=-1.0), INVALID), (orth, dict(eps=NAN), INVALID), (orth, dict(eps=INF), INVALID), (orth, dict(steps=1, ns=[1.0, NAN, 0.0]), INVALID),
     (orth, dict(steps=1, ns=[1.0, 0.0, 1e5]), INVALID), (orth, dict(x=None), INVALID), (orth, dict(out=None), INVALID),
     (orth, dict(x=BUF + 1), MISALIGNED), (orth, dict(t=F32, x=BUF + 2), MISALIGNED), (orth, dict(out=APART + 1), MISALIGNED),
@@ -133,6 +133,10 @@ def test_binding_refusals():
         kw = dict(good, **{name: bad})
         with pytest.raises(ValueError, match=match):
             G.muon_step(plan, [0], 6, 8, kw["master"], kw["momentum"], kw["g"], kw["coef"], hp, kw["params"], None, stream=0)
+    with pytest.raises(ValueError, match="master is required"):
+        G.muon_step(plan, [0], 6, 8, None, good["momentum"], good["g"], good["coef"], hp, good["params"], None, stream=0)
+    with pytest.raises(ValueError, match="make_muon_hp"):
+        G.muon_step(plan, [0], 6, 8, *(good[k] for k in ("master", "momentum", "g", "coef")), G.make_hp(0.1, 0.9, 0.9, 1e-8, 0.1, 1), good["params"], None, stream=0)
     table, s = Dev((32, 2), bf), Dev((1, 2, 3, 4), bf)
     for args, kw, match in (((Dev((64,), bf), s), {}, "2-D"), ((table, Dev((2, 3, 4), bf)), {}, "4-D"), ((table, Dev((1, 3, 3, 4), bf)), {}, "3 heads"),
                             ((table, s), dict(add=Dev((1, 2, 3, 4), f32)), "add has dtype"), ((table, s), dict(add=Dev((1, 2, 3, 5), bf)), "add has 30"),
