@@ -9,7 +9,8 @@
 // result (2-norm) in bf16 and 0.09% in fp16, below bf16's own rounding of the result (0.17%).
 // Range: the singular values of X stay near or below 1.2 with the usual coefficients, so X is
 // held as 2^13 X, and A and S as 2^12 A, 2^12 S.  Values down to 2^-27 (X) and 2^-26 (A, S)
-// then have fp16's full precision, and overflow begins at 8 and 16.  a I is part of S (and
+// then have fp16's full precision, and overflow begins at 8 and 16.  The product of two steps'
+// polynomials is held as 2^8 S1 S0, for values up to 256.  a I is part of S (and
 // not a X added to the product) so that the rounding of S's diagonal is relative to a + b
 // + c after cancellation.
 #pragma once
@@ -20,7 +21,7 @@
 
 namespace {
 
-constexpr float kScaleX = 8192.0f, kScaleA = 4096.0f;
+constexpr float kScaleX = 8192.0f, kScaleA = 4096.0f, kScaleP = 256.0f;
 // Elements a block of the norm and of the scaling takes, 8 a lane.
 constexpr int kUpdateBlock = 256;
 constexpr int64_t kNormTile = 16 * kUpdateBlock;      // two vectors a lane

@@ -130,7 +130,16 @@ int64_t most_parts(int64_t group, const Shape& s) {
 
 Coefficients coefficients(const double* q) { return Coefficients{(float)(q[0] * kScaleA), (float)q[1], (float)(q[2] / kScaleA)}; }
 
-struct Workspace { size_t partial, scale, x[2], a, s, parts, bytes; };
+// Whether two steps go at once: X <- S1 S0 X with A1 = S0 A0 S0 in place of S0 X and (S0 X)(S0 X)^T.
+// That is three symmetric products of the small side for the two of the long one that a step
+// has with X, 3 m^2 (n - m) fewer operations a pair.  By one matrix's sizes, so that a matrix's
+// result does not depend on how many go with it.
+bool in_pairs(const Shape& s) {
+    const int64_t m = s.tall ? s.cols : s.rows, n = s.tall ? s.rows : s.cols;
+    return 2 * n >= 3 * m && m * n >= (int64_t)1 << 20;
+}
+
+struct Workspace { size_t partial, scale, x[2], a, s, t, parts, bytes; };
 Workspace workspace_for(int64_t group, const Shape& s) {
     Workspace w{};
     if (fits_a_block(s)) return w;
@@ -149,6 +158,7 @@ Workspace workspace_for(int64_t group, const Shape& s) {
     for (int k = 0; k < 2; ++k) w.x[k] = take((size_t)2 * group * s.small * s.large);
     w.a = take((size_t)2 * group * s.small * s.small);
     w.s = take((size_t)2 * group * s.small * s.small);
+    if (in_pairs(s)) w.t = take((size_t)2 * group * s.small * s.small);
     w.parts = take(kPartialBytes);
     w.bytes = at;
     return w;
@@ -230,26 +240,54 @@ template <class E>
 int newton_schulz(const char* who, int64_t group, const Shape& s, const Workspace& w, char* base, int steps, const double* ns, const E& last, hipStream_t stream) {
     _Float16* A = reinterpret_cast<_Float16*>(base + w.a);
     _Float16* S = reinterpret_cast<_Float16*>(base + w.s);
+    _Float16* T = reinterpret_cast<_Float16*>(base + w.t);
     void* parts = base + w.parts;
     const int64_t size = s.small * s.large, square = s.small * s.small;
-    const Operand a{A, square, s.small}, p{S, square, s.small};
-    for (int k = 0; k < steps; ++k) {
+    auto small = [&](_Float16* m) { return Operand{m, square, s.small}; };
+    // to = scale l r, symmetric
+    auto multiply = [&](_Float16* l, _Float16* r, _Float16* to, float scale) {
+        return product<false, false>(who, group, small(l), small(r), s.small, s.small, s.small, true, parts, StoreHalf<true>{to, square, s.small, scale}, stream);
+    };
+    auto polynomial = [&](_Float16* of, _Float16* to, const double* q) {
+        const Coefficients f = coefficients(q);
+        return product<false, false>(who, group, small(of), small(of), s.small, s.small, s.small, true, parts,
+                                     StorePolynomial{of, to, square, s.small, f.a, f.b, f.c}, stream);
+    };
+    const bool pairs = in_pairs(s);
+    int rc;
+    for (int k = 0, turn = 0; k < steps; ++turn) {
         const double* q = ns + 3 * k;
-        _Float16* in = reinterpret_cast<_Float16*>(base + w.x[k & 1]);
-        _Float16* out = reinterpret_cast<_Float16*>(base + w.x[~k & 1]);
+        _Float16* in = reinterpret_cast<_Float16*>(base + w.x[turn & 1]);
+        _Float16* out = reinterpret_cast<_Float16*>(base + w.x[~turn & 1]);
         const Operand x{in, size, s.padded_cols};
         const StoreHalf<true> gram{A, square, s.small, kScaleA / (kScaleX * kScaleX)};
-        int rc = s.tall ? product<true, true>(who, group, x, x, s.small, s.small, s.large, true, parts, gram, stream)
-                        : product<false, false>(who, group, x, x, s.small, s.small, s.large, true, parts, gram, stream);
-        if (rc) return rc;
-        const Coefficients f = coefficients(q);
-        const StorePolynomial poly{A, S, square, s.small, f.a, f.b, f.c};
-        if ((rc = product<false, false>(who, group, a, a, s.small, s.small, s.small, true, parts, poly, stream))) return rc;
+        rc = s.tall ? product<true, true>(who, group, x, x, s.small, s.small, s.large, true, parts, gram, stream)
+                    : product<false, false>(who, group, x, x, s.small, s.small, s.large, true, parts, gram, stream);
+        if (rc || (rc = polynomial(A, S, q))) return rc;
+        // of an odd number of steps the one before the last pair goes alone
+        const bool pair = pairs && k + 2 <= steps && !(steps % 2 && k + 3 == steps && steps > 3);
+        _Float16* factor = S;
+        float scale = kScaleA;
+        if (pair) {
+            if ((rc = multiply(S, A, T, 1.0f / kScaleA))) return rc;                                 // S0 A0
+            if ((rc = multiply(S, T, A, 1.0f / kScaleA))) return rc;                                 // A1
+            if ((rc = polynomial(A, T, q + 3))) return rc;                                           // S1
+            if ((rc = multiply(T, S, A, kScaleP / (kScaleA * kScaleA)))) return rc;                  // S1 S0
+            factor = A;
+            scale = kScaleP;
+        }
+        k += pair ? 2 : 1;
         auto apply = [&](const auto& e) {
-            return s.tall ? product<false, false>(who, group, x, p, s.large, s.small, s.small, false, parts, e, stream)
-                          : product<false, true>(who, group, p, x, s.small, s.large, s.small, false, parts, e, stream);
+            return s.tall ? product<false, false>(who, group, x, small(factor), s.large, s.small, s.small, false, parts, e, stream)
+                          : product<false, true>(who, group, small(factor), x, s.small, s.large, s.small, false, parts, e, stream);
         };
-        rc = k + 1 < steps ? apply(StoreHalf<false>{out, size, s.padded_cols, 1.0f / kScaleA}) : apply(last);
+        if (k < steps) {
+            rc = apply(StoreHalf<false>{out, size, s.padded_cols, 1.0f / scale});
+        } else {
+            E e = last;
+            e.scale = 1.0f / (scale * kScaleX);
+            rc = apply(e);
+        }
         if (rc) return rc;
     }
     return GSZ_OK;

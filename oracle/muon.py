@@ -5,31 +5,46 @@ from __future__ import annotations
 import numpy as np
 
 NS = (3.4445, -4.7750, 2.0315)
-SCALE_X, SCALE_A = 2.0 ** 13, 2.0 ** 12      # the library holds 2^13 X, 2^12 A and 2^12 S in fp16
+SCALE_X, SCALE_A, SCALE_P = 2.0 ** 13, 2.0 ** 12, 2.0 ** 8   # the library holds 2^13 X, 2^12 A, 2^12 S and 2^8 S1 S0 in fp16
 
 
 def _half(v, scale):
     return (v * scale).astype(np.float16).astype(np.float64) / scale
 
 
+def in_pairs(rows, cols):
+    """Whether the library takes two steps at once: X <- S1 S0 X, A1 = S0 A0 S0."""
+    m, n = min(rows, cols), max(rows, cols)
+    return m > 128 and (n >= 8 * m or (n >= 3 * m and m * n >= 1 << 20) or (2 * n >= 3 * m and m * n >= 1 << 23))
+
+
 def orthogonalize(x, steps=5, ns=None, eps=1e-7, rounded=False):
     """X = x / (|x| + eps); steps times A = X X^T, X = S X with S = a I + b A + c A A, from the
-    smaller side.  rounded: X, A and S are rounded to fp16 where the library rounds them."""
+    smaller side.  rounded: X, A and S (and what a pair of steps adds) are rounded to fp16 where the
+    library rounds them."""
     x = np.asarray(x, dtype=np.float64)
     if x.shape[0] > x.shape[1]:
         return orthogonalize(x.T, steps, ns, eps, rounded).T
     x = x / (np.sqrt((x * x).sum()) + eps)
-    for k in range(steps):
+    half = _half if rounded else lambda v, scale: v
+    pairs, k = rounded and in_pairs(*x.shape), 0
+
+    def polynomial(A, k):
         a, b, c = NS if ns is None else ns[k]
+        return half(a * np.eye(len(A)) + b * A + c * (A @ A), SCALE_A)
+
+    while k < steps:
         if rounded:
             x = _half(x.astype(np.float32), SCALE_X)
-        A = x @ x.T
-        if rounded:
-            A = _half(A, SCALE_A)
-        S = a * np.eye(len(A)) + b * A + c * (A @ A)
-        if rounded:
-            S = _half(S, SCALE_A)
-        x = S @ x
+        A = half(x @ x.T, SCALE_A)
+        S = polynomial(A, k)
+        if pairs and k + 2 <= steps and not (steps % 2 and k + 3 == steps and steps > 3):
+            A = half(S @ half(S @ A, SCALE_A), SCALE_A)
+            x = half(polynomial(A, k + 1) @ S, SCALE_P) @ x
+            k += 2
+        else:
+            x = S @ x
+            k += 1
     return x
 
 

@@ -84,7 +84,8 @@ def test_many_matrices(count, rows, cols):
         assert torch.equal(run(x[b]), out[b])
 
 
-@pytest.mark.parametrize("count,rows,cols", [(1, 1100, 2300), (9, 1030, 640), (20, 900, 520), (2, 2100, 2000), (26, 64, 3001), (150, 700, 90)])
+@pytest.mark.parametrize("count,rows,cols", [(1, 1100, 2300), (9, 1030, 640), (20, 900, 520), (2, 2100, 2000), (26, 64, 3001), (150, 700, 90),
+                                             (3, 200, 1700), (2, 1700, 150), (1, 600, 2000), (1, 1990, 610), (1, 2300, 3700)])
 def test_large(count, rows, cols):
     """Every size of tiles, last rounds that are cut along the sums, and panels of several matrices."""
     rng = np.random.default_rng(rows)
@@ -109,6 +110,17 @@ def test_steps_and_coefficients(steps):
     check(run(x, steps=steps), x, steps=steps)
     ns = [(1.5, -0.5, 0.0)] * (steps - 1) + [(1.875, -1.25, 0.375)]
     check(run(x, steps=steps, ns=ns), x, steps=steps, ns=ns)
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 5, 6, 7])
+def test_pairs_of_steps(steps):
+    """Long matrices take two steps at once, of an odd number one alone."""
+    assert O.in_pairs(140, 1200) and O.in_pairs(1400, 170)
+    for rows, cols in ((140, 1200), (1400, 170)):
+        x = torch.from_numpy(np.random.default_rng(steps).normal(size=(2, rows, cols))).to(F32).cuda()
+        ns = [(1.5, -0.5, 0.0), (1.875, -1.25, 0.375)] * 4
+        check(run(x, steps=steps, ns=ns[:steps]), x, steps=steps, ns=ns[:steps])
+        check(run(x, steps=steps), x, steps=steps)
 
 
 def test_scale_of_the_input_does_not_matter_and_eps_does():

@@ -90,7 +90,7 @@ def test_workspace_bytes():
         n, small, large = min(count, 256), min(rows, cols), max(rows, cols)
         least = 2 * n * up(small, 32) * up(large, 128) if small <= 128 else 4 * n * (up(rows, 64) * up(cols, 64) + up(small, 64) ** 2)
         assert b % 256 == 0 and least <= b
-        assert b <= least + (4 * n * 128 * 128 if small <= 128 else 0) + (64 << 20) + 8 * n * (rows * cols // 4096 + 2) + 2048
+        assert b <= least + (4 * n * 128 * 128 if small <= 128 else 2 * n * up(small, 64) ** 2) + (64 << 20) + 8 * n * (rows * cols // 4096 + 2) + 2048
         assert b >= G.muon_workspace_bytes(count - 1, rows, cols)
     for rows, cols in ((1, 1), (128, 256), (256, 128), (128, 128)):
         assert G.muon_workspace_bytes(300, rows, cols) == 0

@@ -64,7 +64,7 @@ def test_products(product, form):
 @pytest.mark.parametrize("case", [(1, 1, 1, 1, 5, 1), (2, 5, 9, 0, 5, 2), (1, 9, 5, 1, 3, 3), (2, 130, 40, 1, 2, 4), (1, 33, 300, 0, 2, 5),
                                   (1, 129, 200, 1, 2, 6), (1, 200, 129, 0, 2, 7), (3, 1, 64, 1, 5, 8), (1, 64, 1, 0, 5, 9),
                                   (1, 128, 128, 1, 2, 10), (1, 128, 256, 0, 2, 11), (1, 256, 128, 1, 2, 12), (2, 97, 33, 1, 2, 13),
-                                  (1, 128, 257, 1, 2, 14), (2, 700, 100, 0, 2, 15), (3, 20, 1500, 1, 3, 16), (1, 1, 3000, 0, 5, 17), (1, 300, 1, 1, 5, 18)])
+                                  (1, 128, 257, 1, 2, 14), (2, 700, 100, 0, 2, 15), (3, 20, 1500, 1, 3, 16), (1, 1, 3000, 0, 5, 17), (1, 300, 1, 1, 5, 18), (1, 130, 1100, 1, 3, 19), (1, 1100, 130, 1, 2, 20)])
 def test_orthogonalize(muon, case):
     all_pass(muon, [case])
 
