@@ -50,6 +50,9 @@ __device__ __forceinline__ void interleave() {
     }
 }
 
+// Nothing is scheduled across this place.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
 // What lanes of a wave wrote to LDS is there for its other lanes.
 __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");

@@ -112,5 +112,6 @@ inline f32x16 multiply_add(f16x8 a, f16x8 b, f32x16 acc) {
     });
 }
 template <int READS, int PRODUCTS> inline void interleave() {}
+inline void in_order() {}
 inline void wave_fence() { emu::sync(emu::wave()); }
 }  // namespace
