@@ -1,6 +1,6 @@
 // Matrices with a side of at most 128.  Where both are small, one block does the whole of a
 // matrix: momentum, norm, all Newton-Schulz steps in LDS, and the update.  18 dependent launches of
-// a few microseconds each are what bounds such a matrix otherwise (128 x 128: 75 us, 29 here).
+// a few microseconds each are what bounds such a matrix otherwise (128 x 128: 75 us, 24 here).
 // Where the other side is long, a step is two launches.
 //
 // X lies in LDS as it does in memory, rows of kSmallPitch or 2 kSmallPitch values, and is read both
@@ -212,7 +212,9 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_small(In in, Out out, int 
 // the long side, k = the small side rounded up to 32.  A step is two launches: the blocks of a
 // matrix each take some panels, make S from A for themselves (128^3 products cost less than
 // another launch), replace the panels by S X and add up the new panels' part of A; then those
-// parts are added up.
+// parts are added up.  26 matrices of 64 x 10048: 151 us, ten dependent launches of 10 to 20 us
+// that wait for their panels; as products with their squares 279.  (Pieces of 4 and 8 panels leave
+// too few blocks, and a panel loaded ahead of its use took 171 us.)
 constexpr int kPanel = 128, kPanelPiece = 2;
 struct Panels {
     int rows, cols, k, count, per, parts;    // panels of a matrix; of a block; blocks of a matrix

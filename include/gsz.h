@@ -394,8 +394,12 @@ int gsz_adamw_step(float* master, float* m, float* v, const float* g, int64_t n,
  * (A matrix with more rows than columns goes by X^T X: the same X.)  The products are summed
  * in fp32; X, A and the polynomial are rounded to fp16 between them, scaled by 2^13, 2^12
  * and 2^12, so the iterates' singular values must stay below 4 and the polynomial's values
- * below 16 (the usual coefficients keep them below 1.3 and 3.5).  out is within about 0.2% of
- * the exact result (2-norm), bf16's own rounding included.  A matrix of zeros gives zeros; one with a
+ * below 16 (the usual coefficients keep them below 1.3 and 3.5).  Where one side is well longer, two
+ * steps are worked out together, X <- (S' S) X with A' = S A S, and the product's values must stay
+ * below 256.  Of the exact result (2-norm, bf16's own rounding included) out is off by 0.2% for
+ * matrices of random elements, by up to 0.3% for small ones, 0.5% and 1% where the singular values fall evenly
+ * to 1e-3 and 1e-6 of the largest; directions that x does not have at all but for rounding
+ * grow by 3.4 a step, so a matrix of rank one can be off by 15%.  A matrix of zeros gives zeros; one with a
  * value that is not finite gives NaN everywhere, the others of the call unaffected.
  *   x (device, count * rows * cols values of `type`, GSZ_TYPE_BF16 or GSZ_TYPE_F32, row by
  *     row, one matrix after the other; any multiple of the value's size).

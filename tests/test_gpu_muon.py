@@ -6,7 +6,8 @@ Bounds (2-norm over a matrix), u = 2^-8 the half step of bf16:
   * against the oracle with the same roundings: the kernel's fp32 sums differ from 64-bit ones by
     up to about K 2^-24 of the terms, so a rounding goes the other way where a value lies that close
     to a tie: of K <= 2^11 terms of random sign, about sqrt(K) 2^-24 / 2^-11 < 2^-7 of the values move
-    by a step 2^-10, 2^-10 sqrt(2^-7) < 9e-5 of the norm for each of the 15 roundings, grown by at most
+    by a step 2^-10, 2^-10 sqrt(2^-7) < 9e-5 of the norm for each of the 15 roundings (17 where steps go
+    in pairs), grown by at most
     3.5 a step (sum over steps of 3 * 3.5^(4 - k) < 630 in the first order's worst case, about 10 where
     the change is spread over all directions): 1e-3 for the fp32 result; for bf16 1e-3 of change
     moves 1e-3 / 2^-8 < 26% of the roundings by 2^-7 at most: sqrt(0.26) 2^-8 < 2e-3 more.
