@@ -59,7 +59,7 @@ bool overlap(Span a, Span b) {
     return a.p && b.p && a.bytes > 0 && b.bytes > 0 && (x < y ? y - x < (uintptr_t)a.bytes : x - y < (uintptr_t)b.bytes);
 }
 
-// Sizes of a call.  All products of them fit 62 bits.
+// Sizes of a call.  Where none is 0 all products of them fit 62 bits.
 int check_sizes(const char* who, int64_t batch, int64_t heads, int64_t q, int64_t k, int64_t buckets) {
     if (batch < 0 || heads < 0 || q < 0 || k < 0) return bad_arg(who, "negative size");
     constexpr int64_t kMost = (int64_t)1 << 30;
@@ -110,6 +110,7 @@ int check_start(const char* who, int64_t q_start, const void* starts, int32_t st
     return GSZ_OK;
 }
 
+int64_t scores(int64_t batch, int64_t heads, int64_t q, int64_t k) { return batch && heads && q && k ? batch * heads * q * k : 0; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int grid_for(int64_t tiles, int block) {
     const int64_t cap = kMaxWorkItems / block;
@@ -200,7 +201,7 @@ extern "C" int gsz_relpos_bias(const void* table, int32_t table_type, int64_t bu
     if ((rc = check_start(who, q_start, q_starts, start_type, &start))) return rc;
     const float c = (float)scale;
     if (!std::isfinite(c)) return bad_arg(who, "scale is not finite in fp32");
-    const int64_t n = batch * heads * q_len * k_len;
+    const int64_t n = scores(batch, heads, q_len, k_len);
     if (n > 0 && (!table || !out)) return bad_arg(who, "NULL buffer");
     if (off_by(table, ts) || off_by(out, os) || off_by(add, os)) { set_error("%s: a buffer is not aligned to its values", who); return GSZ_ERR_MISALIGNED; }
     const Span written{out, n * os};
@@ -254,7 +255,7 @@ extern "C" int gsz_relpos_bias_grad(const void* dy, int32_t dy_type, int64_t buc
     RelStart start;
     if ((rc = check_start(who, q_start, q_starts, start_type, &start))) return rc;
     if (!std::isfinite((float)scale)) return bad_arg(who, "scale is not finite in fp32");
-    const int64_t n = batch * heads * q_len * k_len;
+    const int64_t n = scores(batch, heads, q_len, k_len);
     if ((n > 0 && !dy) || (heads > 0 && !grad)) return bad_arg(who, "NULL buffer");
     if (off_by(dy, ds) || off_by(grad, gs)) { set_error("%s: a buffer is not aligned to its values", who); return GSZ_ERR_MISALIGNED; }
     int block = 64;

@@ -131,12 +131,18 @@ int64_t most_parts(int64_t group, const Shape& s) {
 Coefficients coefficients(const double* q) { return Coefficients{(float)(q[0] * kScaleA), (float)q[1], (float)(q[2] / kScaleA)}; }
 
 // Whether two steps go at once: X <- S1 S0 X with A1 = S0 A0 S0 in place of S0 X and (S0 X)(S0 X)^T.
-// That is three symmetric products of the small side for the two of the long one that a step
-// has with X, 3 m^2 (n - m) fewer operations a pair.  By one matrix's sizes, so that a matrix's
-// result does not depend on how many go with it.
-bool in_pairs(const Shape& s) {
+// That is three more symmetric products of the small side for the two of the long one that a step has
+// with X: 3 m^2 (n - m) fewer operations a pair and matrix, and a launch more.  Where those operations
+// outweigh it, measured one at a time and in pairs (us for five steps):
+//   n >= 8 m: 1 x 129 x 4000 132, 121; 1 x 384 x 3136 144, 136; 20 x 200 x 2000 182, 162
+//   n >= 2.5 m: 1 x 768 x 2304 169, 170; 4 x 640 x 1664 175, 171; 1 x 1024 x 4096 235, 224;
+//     16 x 640 x 1664 422, 379; 12 x 768 x 2304 510, 449; but 8 x 256 x 1024 110, 112
+//   n >= 1.5 m: 24 x 1024 x 1536 1024, 983; but 1 x 1024 x 2048 176, 189; 1 x 2048 x 3200 482, 502;
+//     5 x 777 x 1531 245, 250
+bool in_pairs(int64_t group, const Shape& s) {
     const int64_t m = s.tall ? s.cols : s.rows, n = s.tall ? s.rows : s.cols;
-    return 2 * n >= 3 * m && m * n >= (int64_t)1 << 20;
+    const int64_t saved = group * m * m * (n - m);
+    return n >= 8 * m || (2 * n >= 5 * m && saved >= (int64_t)1 << 30) || (2 * n >= 3 * m && saved >= (int64_t)1 << 33);
 }
 
 struct Workspace { size_t partial, scale, x[2], a, s, t, parts, bytes; };
@@ -158,7 +164,7 @@ Workspace workspace_for(int64_t group, const Shape& s) {
     for (int k = 0; k < 2; ++k) w.x[k] = take((size_t)2 * group * s.small * s.large);
     w.a = take((size_t)2 * group * s.small * s.small);
     w.s = take((size_t)2 * group * s.small * s.small);
-    if (in_pairs(s)) w.t = take((size_t)2 * group * s.small * s.small);
+    if (in_pairs(group, s)) w.t = take((size_t)2 * group * s.small * s.small);
     w.parts = take(kPartialBytes);
     w.bytes = at;
     return w;
@@ -253,7 +259,7 @@ int newton_schulz(const char* who, int64_t group, const Shape& s, const Workspac
         return product<false, false>(who, group, small(of), small(of), s.small, s.small, s.small, true, parts,
                                      StorePolynomial{of, to, square, s.small, f.a, f.b, f.c}, stream);
     };
-    const bool pairs = in_pairs(s);
+    const bool pairs = in_pairs(group, s);
     int rc;
     for (int k = 0, turn = 0; k < steps; ++turn) {
         const double* q = ns + 3 * k;

@@ -394,12 +394,12 @@ int gsz_adamw_step(float* master, float* m, float* v, const float* g, int64_t n,
  * (A matrix with more rows than columns goes by X^T X: the same X.)  The products are summed
  * in fp32; X, A and the polynomial are rounded to fp16 between them, scaled by 2^13, 2^12
  * and 2^12, so the iterates' singular values must stay below 4 and the polynomial's values
- * below 16 (the usual coefficients keep them below 1.3 and 3.5).  Where one side is well longer, two
- * steps are worked out together, X <- (S' S) X with A' = S A S, and the product's values must stay
- * below 256.  Of the exact result (2-norm, bf16's own rounding included) out is off by 0.2% for
- * matrices of random elements, by up to 0.3% for small ones, 0.5% and 1% where the singular values fall evenly
- * to 1e-3 and 1e-6 of the largest; directions that x does not have at all but for rounding
- * grow by 3.4 a step, so a matrix of rank one can be off by 15%.  A matrix of zeros gives zeros; one with a
+ * below 16 (the usual coefficients keep them below 1.3 and 3.5).  Where one side is well
+ * longer (how much goes by the sizes and by count) two steps are worked out together, X <- (S' S) X
+ * with A' = S A S, and the product's values must stay below 256.  Of the exact result (2-norm, bf16's own rounding included) out is off by 0.2% for
+ * matrices of random elements, by up to 0.3% for small ones, 0.5% and 1% where the singular values
+ * fall evenly to 1e-3 and 1e-6 of the largest; directions that x does not have at all but for
+ * rounding grow by 3.4 a step, so a matrix of rank one can be off by 15%.  A matrix of zeros gives zeros; one with a
  * value that is not finite gives NaN everywhere, the others of the call unaffected.
  *   x (device, count * rows * cols values of `type`, GSZ_TYPE_BF16 or GSZ_TYPE_F32, row by
  *     row, one matrix after the other; any multiple of the value's size).
@@ -418,8 +418,8 @@ int gsz_orthogonalize(const void* x, int32_t type, int64_t count, int64_t rows, 
 
 /* *out = bytes of device scratch that gsz_orthogonalize and gsz_muon_step need for `count`
  * matrices of rows x cols, or fewer: none for matrices of at most 128 by 256 (or 256 by 128); else, for
- * at most 256 matrices at a time (fewer where they hold 2^33 elements), about 4 bytes an element (2 where the smaller side is at most
- * 128), 4 per element of a square of the smaller side, and up to 64 MiB for products cut along
+ * at most 256 matrices at a time (fewer where they hold 2^33 elements), about 4 bytes an element (2 where
+ * the smaller side is at most 128), 6 per element of a square of the smaller side, and up to 64 MiB for products cut along
  * their sums.  Sides count rounded up to 64 (a long one beside a side of at most 128 to 128).
  * Needs no initialisation. */
 int gsz_muon_workspace_bytes(int64_t count, int64_t rows, int64_t cols, size_t* out);

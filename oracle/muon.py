@@ -12,22 +12,23 @@ def _half(v, scale):
     return (v * scale).astype(np.float16).astype(np.float64) / scale
 
 
-def in_pairs(rows, cols):
-    """Whether the library takes two steps at once: X <- S1 S0 X, A1 = S0 A0 S0."""
+def in_pairs(rows, cols, count=1):
+    """Whether the library takes two steps at once (X <- S1 S0 X, A1 = S0 A0 S0) for `count` matrices."""
     m, n = min(rows, cols), max(rows, cols)
-    return m > 128 and (n >= 8 * m or (n >= 3 * m and m * n >= 1 << 20) or (2 * n >= 3 * m and m * n >= 1 << 23))
+    saved = count * m * m * (n - m)
+    return m > 128 and (n >= 8 * m or (2 * n >= 5 * m and saved >= 1 << 30) or (2 * n >= 3 * m and saved >= 1 << 33))
 
 
-def orthogonalize(x, steps=5, ns=None, eps=1e-7, rounded=False):
+def orthogonalize(x, steps=5, ns=None, eps=1e-7, rounded=False, count=1):
     """X = x / (|x| + eps); steps times A = X X^T, X = S X with S = a I + b A + c A A, from the
     smaller side.  rounded: X, A and S (and what a pair of steps adds) are rounded to fp16 where the
-    library rounds them."""
+    library rounds them in a call of `count` such matrices."""
     x = np.asarray(x, dtype=np.float64)
     if x.shape[0] > x.shape[1]:
-        return orthogonalize(x.T, steps, ns, eps, rounded).T
+        return orthogonalize(x.T, steps, ns, eps, rounded, count).T
     x = x / (np.sqrt((x * x).sum()) + eps)
     half = _half if rounded else lambda v, scale: v
-    pairs, k = rounded and in_pairs(*x.shape), 0
+    pairs, k = rounded and in_pairs(*x.shape, count), 0
 
     def polynomial(A, k):
         a, b, c = NS if ns is None else ns[k]

@@ -52,9 +52,11 @@ def run(x, **kw):
     return out
 
 
-def check(out, x, **kw):
+def check(out, x, count=None, **kw):
+    """count: how many matrices the call had, where out and x are only some of them."""
+    count = count or (1 if x.dim() == 2 else x.shape[0])
     for got, xi in zip(f64(out).reshape(-1, *out.shape[-2:]), f64(x).reshape(-1, *x.shape[-2:])):
-        exact, same = O.orthogonalize(xi, **kw), O.orthogonalize(xi, rounded=True, **kw)
+        exact, same = O.orthogonalize(xi, **kw), O.orthogonalize(xi, rounded=True, count=count, **kw)
         d = norm(got - exact)
         assert d <= 2 * O.rounding_bound(xi, **kw) + U * norm(exact), d / norm(exact)
         d = norm(got - same.astype(np.float32))
@@ -79,20 +81,21 @@ def test_many_matrices(count, rows, cols):
     x = torch.from_numpy(rng.normal(0, 1, (count, rows, cols)) * 10.0 ** rng.uniform(-6, 6, (count, 1, 1))).to(F32).cuda()
     out = run(x)
     some = [0, 1, count // 2, count - 2, count - 1]
-    check(out[some], x[some])
+    check(out[some], x[some], count)
     # each by itself gives the same bits
     for b in some[::2]:
         assert torch.equal(run(x[b]), out[b])
 
 
 @pytest.mark.parametrize("count,rows,cols", [(1, 1100, 2300), (9, 1030, 640), (20, 900, 520), (2, 2100, 2000), (26, 64, 3001), (150, 700, 90),
-                                             (3, 200, 1700), (2, 1700, 150), (1, 600, 2000), (1, 1990, 610), (1, 2300, 3700)])
+                                             (3, 200, 1700), (2, 1700, 150), (1, 600, 2000), (1, 1990, 610), (1, 2300, 3700),
+                                             (12, 400, 1100), (25, 1400, 900)])
 def test_large(count, rows, cols):
     """Every size of tiles, last rounds that are cut along the sums, and panels of several matrices."""
     rng = np.random.default_rng(rows)
     x = torch.from_numpy(rng.normal(0, 1, (count, rows, cols))).to(F32).cuda()
     out = run(x)
-    check(out[[0, count - 1]], x[[0, count - 1]])
+    check(out[[0, count - 1]], x[[0, count - 1]], count)
 
 
 def test_low_rank_and_wide_spectrum():
@@ -116,7 +119,8 @@ def test_steps_and_coefficients(steps):
 @pytest.mark.parametrize("steps", [1, 2, 3, 4, 5, 6, 7])
 def test_pairs_of_steps(steps):
     """Long matrices take two steps at once, of an odd number one alone."""
-    assert O.in_pairs(140, 1200) and O.in_pairs(1400, 170)
+    assert O.in_pairs(140, 1200) and O.in_pairs(1400, 170) and O.in_pairs(400, 1100, 12) and O.in_pairs(1400, 900, 25)
+    assert not (O.in_pairs(400, 1100) or O.in_pairs(1400, 900))
     for rows, cols in ((140, 1200), (1400, 170)):
         x = torch.from_numpy(np.random.default_rng(steps).normal(size=(2, rows, cols))).to(F32).cuda()
         ns = [(1.5, -0.5, 0.0), (1.875, -1.25, 0.375)] * 4
@@ -208,7 +212,7 @@ def test_update(rows, cols, numel, tensors, nesterov):
         assert np.array_equal(m1[s], want)
         if t in tensors[:3] + tensors[-3:]:
             u = (gc + f(MU) * want if nesterov else want).reshape(rows, cols)
-            same = O.orthogonalize(u, rounded=True)
+            same = O.orthogonalize(u, rounded=True, count=len(tensors))
             exact = O.orthogonalize(u)
             got = (w0[s].astype(np.float64) * float(f(1 - LR * WD)) - w1[s]).reshape(rows, cols) / float(f(LR * scale))
             # the update's own roundings: theta to fp32 three times, 2^-24 of it each
