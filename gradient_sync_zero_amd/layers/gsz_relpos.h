@@ -123,9 +123,14 @@ template <> struct Wide<float> {
     }
 };
 
-// NT: nontemporal accesses, for scores of 64 MiB and more that are added to and whose rows begin at
-// multiples of 16 bytes (4 x 32 heads of 2048 x 2048 bf16 391 us against 407, 2 x 32 of 4096 x 4096
-// 723 against 760; but 946 against 906 for 4096 x 4095, and 376 against 360 with nothing to add to).
+// NT: nontemporal accesses, for more than 128 MiB of scores that are added to, in whole lines of 128
+// bytes from a multiple of 64 on.  In us, with them and without:
+//   4 x 32 heads of 2048 x 2048 bf16 390, 406; 64 bytes on 408, 415; 16 bytes on 452, 417
+//   2 x 32 of 4096 x 4096 727, 757; 8 x 32 of 1024 x 2112 423, 441; 2 x 12 of 2048 x 2048 80, 84
+//   rows that are no whole lines: 8 x 32 of 1024 x 2080 457, 443; x 2064 550, 467
+//   128 MiB (1 x 16 of 2048 x 2048) 58, 62, but added to in place 58, 46: the last-level cache holds it
+//   with nothing to add to, 4 x 32 of 2048 x 2048: 376, 360
+// (Buffer descriptors with nontemporal or sc1 stores, 400 and more for the first.)
 template <typename T, typename O, bool ADD, bool NT>
 __global__ __launch_bounds__(kRelBlock) void k_relpos_bias(const T* table, RelMap map, RelStart start, BiasShape s, float scale,
                                                            const O* add, O* out) {

@@ -213,7 +213,7 @@ extern "C" int gsz_relpos_bias(const void* table, int32_t table_type, int64_t bu
     int block;
     const BiasShape s = bias_shape(batch, heads, q_len, k_len, buckets, 16 / (int)os, &block);
     const int grid = grid_for(s.tiles, block);
-    const bool stream_past = n * os >= (int64_t)64 << 20 && k_len * os % 16 == 0 && !off_by(add, 16) && !off_by(out, 16);
+    const bool stream_past = n * os > (int64_t)128 << 20 && k_len * os % 128 == 0 && !off_by(add, 64) && !off_by(out, 64);
     with_type(table_type, [&](auto t) {
         with_type(out_type, [&](auto o) {
             with_bool(add != nullptr, [&](auto a) {

@@ -180,3 +180,68 @@ def test_capture_and_other_streams():
         both()
     torch.cuda.synchronize()
     assert torch.equal(out, got[0]) and torch.equal(g, got[1])
+
+
+def line(table, q, k, far, both, start):
+    """(heads, q + k - 1): the oracle's bias by diagonal, from j - i = 1 - q on."""
+    d = np.arange(1 - q, k) - start
+    return torch.from_numpy(f64(table)[O.bucket(d, table.shape[0], far, both)].T.copy()).float().cuda()
+
+
+def rows_of(lines, q, k, i0, i1):
+    """(heads, i1 - i0, k) of the bias."""
+    at = torch.arange(k, device="cuda")[None] - torch.arange(i0, i1, device="cuda")[:, None] + q - 1
+    return lines[:, at]
+
+
+@pytest.mark.parametrize("batch,heads,q,k,dtype,shift", [
+    (2, 17, 1025, 2112, BF, 0), (2, 17, 1025, 2112, BF, 32), (2, 17, 1025, 2112, BF, 8), (1, 9, 2050, 2080, F32, 16),
+    (3, 11, 1030, 2060, BF, 0), (1, 16, 2048, 2048, BF, 0)])
+def test_scores_past_the_caches(batch, heads, q, k, dtype, shift):
+    """More than 128 MiB and just that, in whole lines and not.  Half-integers and one rounding: exact."""
+    rng = np.random.default_rng(k)
+    table = torch.from_numpy(rng.integers(-8, 9, (32, heads)) / 2).to(BF).cuda()
+    lines = line(table, q, k, 128, True, 3)
+    n = batch * heads * q * k
+    add = torch.randn(n + 64, device="cuda").to(dtype)[shift:shift + n].view(batch, heads, q, k)
+    out = Guarded((batch, heads, q, k), dtype, shift)
+    G.relpos_bias(table, out.t, 128, True, q_start=3, add=add)
+    out.check()
+    want = (add.float() + rows_of(lines, q, k, 0, q)).to(dtype)
+    assert torch.equal(out.t, want)
+    G.relpos_bias(table, add, 128, True, q_start=3, add=add)
+    assert torch.equal(add, want)
+
+
+@pytest.mark.parametrize("k,shift", [(16384, 0), (16381, 3)])
+def test_offsets_past_32_bits(k, shift):
+    """Over 2^32 bytes and over 2^31 scores; the gradient's sums are of small whole numbers: exact but
+    for the output's rounding."""
+    heads, q = 9, 16400
+    n = heads * q * k
+    assert n > 2 ** 31
+    table = torch.from_numpy(np.random.default_rng(k).integers(-8, 9, (32, heads)) / 2).to(BF).cuda()
+    lines = line(table, q, k, 128, False, 0)
+    add = torch.empty(n + 8, device="cuda", dtype=BF)[shift:shift + n].view(1, heads, q, k)
+    add.random_(-2, 3)
+    keep = add.clone()
+    grad = torch.full((32, heads), 0.5, device="cuda")
+    ws = torch.empty(G.relpos_bias_workspace_bytes(1, heads, q, k, 32), dtype=torch.uint8, device="cuda")
+    G.relpos_bias_grad(add, grad, ws, 128, False, accumulate=True)
+    assert torch.equal(add, keep)
+    G.relpos_bias(table, add, 128, False, add=add)
+    first = torch.tensor(O.borders(32, 128, False), device="cuda")
+    total = torch.zeros(heads, 32, dtype=torch.int64, device="cuda")
+    for i in range(0, q, 400):
+        to = min(q, i + 400)
+        assert torch.equal(add[0, :, i:to], (keep[0, :, i:to].float() + rows_of(lines, q, k, i, to)).to(BF)), i
+        # a bucket's columns of a row: distances first[b] to first[b + 1] - 1 to the left, bucket 0 all to the right
+        sums = torch.zeros(heads, to - i, k + 1, dtype=torch.int32, device="cuda")
+        sums[:, :, 1:] = keep[0, :, i:to].int().cumsum(2, dtype=torch.int32)
+        end = (torch.arange(i, to, device="cuda")[:, None] + 1 - first[None]).clamp(0, k)
+        end[:, 0] = k
+        begin = torch.cat([end[:, 1:], torch.zeros_like(end[:, :1])], 1)
+        begin[:, 0] = torch.arange(i, to, device="cuda").clamp(0, k)
+        pick = lambda at: sums.gather(2, at[None].expand(heads, -1, -1))  # noqa: E731
+        total += (pick(end) - pick(begin)).sum(1)
+    assert torch.equal(grad, (total.T + 0.5).float())
