@@ -277,3 +277,37 @@ def test_capture_and_other_streams():
             G.orthogonalize(x[k], outs[k], spaces[k], stream=streams[k])
     torch.cuda.synchronize()
     assert torch.equal(outs[0], alone[0]) and torch.equal(outs[1], alone[1])
+
+
+@pytest.mark.parametrize("rows,cols", [(2 ** 17, 16400), (16400, 2 ** 17)])
+def test_offsets_past_32_bits(rows, cols):
+    """Over 2^31 elements and 2^32 bytes: signs (-1)^popcount(i & j), whose columns (rows) are orthogonal,
+    so that every singular value is the same and the result is x times a number, f(f(f(f(f(s))))).
+    A rounding, off by h = 2^-11, of X, A or S (three a step, in pairs fewer than four) changes a
+    step's result by at most h (|a| s + 3 |b| s^3 + 5 |c| s^5), and the later steps that by s f'/f
+    each; doubled for what lies beyond the first order, and u for the output."""
+    n, m = max(rows, cols), min(rows, cols)
+    assert rows * cols > 2 ** 31
+
+    def signs(i0, i1):
+        v = torch.arange(i0, i1, device="cuda", dtype=torch.int32)[:, None] & torch.arange(cols, device="cuda", dtype=torch.int32)[None]
+        for shift in (16, 8, 4, 2, 1):
+            v = v ^ (v >> shift)
+        return (1 - 2 * (v & 1)).to(BF)
+
+    x = torch.empty(rows, cols, dtype=BF, device="cuda")
+    step = 2 ** 26 // cols
+    for i in range(0, rows, step):
+        x[i:i + step] = signs(i, min(rows, i + step))
+    ws = torch.empty(G.muon_workspace_bytes(1, rows, cols), dtype=torch.uint8, device="cuda")
+    G.orthogonalize(x, x, ws)
+    a, b, c = O.NS
+    s, off = m ** -0.5, 0.0
+    for _ in range(5):
+        f = a * s + b * s ** 3 + c * s ** 5
+        off = off * abs(s * (a + 3 * b * s ** 2 + 5 * c * s ** 4) / f) + 4 * 2.0 ** -11 * (a * s + 3 * abs(b) * s ** 3 + 5 * c * s ** 5) / abs(f)
+        s = f
+    want = s * n ** -0.5
+    for i in range(0, rows, step):
+        got = x[i:i + step].float() * signs(i, min(rows, i + step)).float() / want
+        assert float((got - 1).abs().max()) <= 2 * off + U, (i, 2 * off)
