@@ -771,6 +771,7 @@ def make_muon_hp(lr, momentum=0.95, weight_decay=0.0, scale=1.0, nesterov=True, 
     hp = MuonHP(lr, momentum, weight_decay, scale, eps, None, steps, 1 if nesterov else 0)
     if ns is not None:
         hp.ns = _coefficients(ns, steps)            # the structure keeps the array alive
+        hp.ns_steps = steps
     return hp
 
 
@@ -798,6 +799,8 @@ def muon_step(plan, tensors, rows, cols, master, momentum, g, coef, hp, params, 
     sp, nbytes = _workspace(ws, dev)
     if not isinstance(hp, MuonHP):
         raise ValueError("hp must come from make_muon_hp")
+    if hp.ns and getattr(hp, "ns_steps", None) != hp.steps:
+        raise ValueError("hp.steps or hp.ns was changed: make_muon_hp takes both")
     rc = lib.gsz_muon_step(plan.handle, arr, count, rows, cols, wp, mp, gp, cp, ctypes.byref(hp), pp, sp, nbytes,
                            _layer_stream(stream, dev))
     if rc:

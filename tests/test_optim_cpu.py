@@ -137,6 +137,11 @@ def test_binding_refusals():
         G.muon_step(plan, [0], 6, 8, None, good["momentum"], good["g"], good["coef"], hp, good["params"], None, stream=0)
     with pytest.raises(ValueError, match="make_muon_hp"):
         G.muon_step(plan, [0], 6, 8, *(good[k] for k in ("master", "momentum", "g", "coef")), G.make_hp(0.1, 0.9, 0.9, 1e-8, 0.1, 1), good["params"], None, stream=0)
+    # coefficients of fewer steps than the call would read
+    longer = G.make_muon_hp(0.1, steps=2, ns=[(1.5, -0.5, 0.0)] * 2)
+    longer.steps = 5
+    with pytest.raises(ValueError, match="was changed"):
+        G.muon_step(plan, [0], 6, 8, *(good[k] for k in ("master", "momentum", "g", "coef")), longer, good["params"], None, stream=0)
     table, s = Dev((32, 2), bf), Dev((1, 2, 3, 4), bf)
     for args, kw, match in (((Dev((64,), bf), s), {}, "2-D"), ((table, Dev((2, 3, 4), bf)), {}, "4-D"), ((table, Dev((1, 3, 3, 4), bf)), {}, "3 heads"),
                             ((table, s), dict(add=Dev((1, 2, 3, 4), f32)), "add has dtype"), ((table, s), dict(add=Dev((1, 2, 3, 5), bf)), "add has 30"),
