@@ -206,7 +206,8 @@ __global__ __launch_bounds__(64 * F::kWaves) void k_product(Operand L, Operand R
         __syncthreads();
         next_tile();
         // The next loads go out between the products, a few after each: all of them first kept the
-        // matrix cores waiting (8192 cubed 881 -> 850 us, 12 x 768 x 2304 x 768 45.0 -> 42.8).
+        // matrix cores waiting (8192 cubed 881 -> 850 us, 12 x 768 x 2304 x 768 45.0 -> 42.8; in the
+        // first half of the products only 866, a wave's priority raised while it multiplies 890).
         // Where a wave has one product they go first (5 x 832 x 832 x 1536 14.4, after it 15.0).
         constexpr int kProducts = FM * FN;
         if constexpr (kProducts == 1) {
