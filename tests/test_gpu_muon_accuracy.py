@@ -1,0 +1,48 @@
+"""Spectra and ranks of the orthogonalised matrix on the GPU, in every form of the kernels.
+
+Bounds (2-norm), u = 2^-8 the half step of bf16, r = oracle.muon.rounding_bound:
+  * against the exact result: 2 r (what a call gives is about 0.7 r, and 1.8 r where a single value
+    is rounded), and u |O| for the output;
+  * against the oracle with the same roundings: of sums of K <= 500 terms in fp32 a part of at most
+    K 2^-24 / 2^-11 < 1 / 12 lies so close to a tie that it is rounded the other way, by a step, whose mean
+    square is 12 times a rounding's: r for the fp32 result, and 2 u |O| for outputs rounded
+    apart.
+"""
+import numpy as np
+import pytest
+import torch
+
+import gradient_sync_zero_amd as G
+from oracle import muon as O
+from tests.test_gpu_muon import f64, norm, run, workspace
+from tests.test_muon_accuracy import NAMES, U, matrix
+
+pytestmark = pytest.mark.gpu
+
+
+# one block (both orientations), panels, products in tiles of 64, in pairs, tall
+@pytest.mark.parametrize("rows,cols", [(60, 100), (128, 128), (250, 120), (90, 400), (500, 100), (160, 200), (300, 257), (140, 1200), (1200, 140)])
+@pytest.mark.parametrize("name", NAMES)
+def test_spectra(rows, cols, name):
+    x = torch.from_numpy(matrix(rows, cols, name)).cuda()
+    out = f64(run(x))
+    exact, r = O.orthogonalize(f64(x)), O.rounding_bound(f64(x))
+    assert norm(out - exact) <= 2 * r + U * norm(exact), (norm(out - exact) / norm(exact), r / norm(exact))
+    same = O.orthogonalize(f64(x), rounded=True)
+    assert norm(out - same) <= r + 2 * U * norm(same), norm(out - same) / norm(same)
+
+
+@pytest.mark.parametrize("rows,cols", [(60, 100), (90, 400), (160, 200), (1200, 140)])
+@pytest.mark.parametrize("name", NAMES)
+def test_updates(rows, cols, name):
+    """The weights of an update, whose direction is the gradient: O is not rounded to bf16."""
+    u = matrix(rows, cols, name)
+    plan = G.Plan([11, rows * cols], 1 << 40, 1)
+    w, m, g = (torch.zeros(plan.flat_len, device="cuda") for _ in range(3))
+    p = torch.zeros(plan.flat_len, dtype=torch.bfloat16, device="cuda")
+    plan.view(1, g).copy_(torch.from_numpy(u).cuda().view(-1))
+    hp = G.make_muon_hp(lr=1.0, momentum=0.0, scale=-1.0, nesterov=False)
+    G.muon_step(plan, [1], rows, cols, w, m, g, torch.ones(1, device="cuda"), hp, p, workspace(1, rows, cols))
+    got, exact = f64(plan.view(1, w)).reshape(rows, cols), O.orthogonalize(u)
+    assert norm(got - exact) <= 2 * O.rounding_bound(u), norm(got - exact) / norm(exact)
+    assert norm(got - O.orthogonalize(u, rounded=True)) <= O.rounding_bound(u)

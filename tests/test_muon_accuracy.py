@@ -1,0 +1,105 @@
+"""What oracle.muon.rounding_bound says against what the fp16 roundings do, and that a result with a
+mistake in it is outside of the tolerances built on it (2 rounding_bound for fp32 results, half a
+step of bf16 more for bf16 ones)."""
+import numpy as np
+import pytest
+
+from oracle import muon
+
+U = 2.0 ** -8
+
+
+def norm(x):
+    return float(np.sqrt((np.asarray(x) ** 2).sum()))
+
+
+def spectrum(name, m):
+    if name == "1e-3" or name == "1e-6":
+        return 10.0 ** -np.linspace(0, float(name[3:]), m)
+    return np.r_[np.ones(int(name)), np.zeros(m - int(name))]
+
+
+def matrix(rows, cols, name, seed=1):
+    """Random elements, singular values that fall evenly, or `name` equal ones and zeros."""
+    rng = np.random.default_rng(seed)
+    if name == "random":
+        return rng.normal(size=(rows, cols)).astype(np.float32)
+    m = min(rows, cols)
+    u, v = np.linalg.qr(rng.normal(size=(rows, m)))[0], np.linalg.qr(rng.normal(size=(cols, m)))[0]
+    return ((u * spectrum(name, m)) @ v.T).astype(np.float32)
+
+
+NAMES = ["random", "1e-3", "1e-6", "1", "4", "8"]
+
+
+@pytest.mark.parametrize("rows,cols", [(17, 64), (60, 100), (160, 200), (500, 200), (140, 1200)])
+@pytest.mark.parametrize("name", NAMES)
+def test_the_bound_is_near_what_the_roundings_do(rows, cols, name):
+    """Each error is at most 1 and at least 1 / 2 of its part of the bound (the mean square of
+    4^e / v^2, v in [2^e, 2^(e + 1)), is between 1 / 4 and 1), and pairs count one error twice."""
+    x = matrix(rows, cols, name)
+    off = norm(muon.orthogonalize(x, rounded=True) - muon.orthogonalize(x))
+    assert 0.4 < off / muon.rounding_bound(x) < 1.0
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 7), (5, 1), (2, 3), (4, 4), (1, 3001), (9, 5)])
+def test_few_values(rows, cols):
+    """A rounding alone is at most sqrt(3) of its mean square's root."""
+    for seed in range(20):
+        x = matrix(rows, cols, "random", seed)
+        assert norm(muon.orthogonalize(x, rounded=True) - muon.orthogonalize(x)) <= 2 * muon.rounding_bound(x)
+
+
+@pytest.mark.parametrize("steps,ns", [(1, None), (3, None), (16, None), (4, [(1.5, -0.5, 0.0)] * 3 + [(1.875, -1.25, 0.375)])])
+@pytest.mark.parametrize("rows,cols", [(70, 150), (140, 1200)])
+def test_other_steps(rows, cols, steps, ns):
+    x = matrix(rows, cols, "random")
+    off = norm(muon.orthogonalize(x, steps, ns, rounded=True) - muon.orthogonalize(x, steps, ns))
+    bound = muon.rounding_bound(x, steps, ns)
+    assert 0.1 * bound < off <= bound
+
+
+def test_nothing_and_too_much():
+    assert muon.rounding_bound(np.zeros((3, 4))) == 0.0
+    with pytest.raises(ValueError, match="range"), np.errstate(all="ignore"):
+        muon.rounding_bound(np.eye(3), 16, [(1e4, 1e4, 1e4)] * 16)
+
+
+def bf16(v):
+    w = np.ascontiguousarray(v, dtype=np.float32).view(np.uint32)
+    return ((w + 0x7FFF + (w >> 16 & 1)) & np.uint32(0xFFFF0000)).view(np.float32).astype(np.float64)
+
+
+@pytest.mark.parametrize("rows,cols", [(48, 96), (60, 100), (128, 128), (200, 500)])
+def test_a_mistake_is_seen(rows, cols):
+    x = matrix(rows, cols, "random")
+    exact, good = muon.orthogonalize(x), muon.orthogonalize(x, rounded=True)
+    update = 2 * muon.rounding_bound(x)
+    out = update + U * norm(exact)
+    assert norm(good - exact) <= update and norm(bf16(good) - exact) <= out
+    a, b, c = muon.NS
+    for wrong in (muon.orthogonalize(x, steps=4, rounded=True), muon.orthogonalize(x, ns=[(a, b, 1.02 * c)] * 5, rounded=True)):
+        assert norm(bf16(wrong) - exact) > out
+    part = bf16(good)
+    part[-5:] = 0.0                                      # rows past the last whole tile left out
+    assert norm(part - exact) > out
+    part = bf16(good)
+    part[0, 0] = np.nan
+    assert not norm(part - exact) <= out
+    assert norm(muon.orthogonalize(x, ns=[(a, b, 1.005 * c)] * 5) - exact) > update
+    coarse = x.astype(np.float64) / norm(x)              # the iterates held in bf16
+    for _ in range(5):
+        coarse = bf16(coarse)
+        A = bf16(coarse @ coarse.T)
+        coarse = bf16(a * np.eye(rows) + b * A + c * A @ A) @ coarse
+    assert norm(coarse - exact) > update
+
+
+@pytest.mark.parametrize("name", ["1e-3", "1e-6", "1", "8"])
+def test_a_mistake_is_seen_in_other_spectra(name):
+    x = matrix(60, 100, name)
+    exact, a = muon.orthogonalize(x), muon.NS[0]
+    out = 2 * muon.rounding_bound(x) + U * norm(exact)
+    assert norm(bf16(muon.orthogonalize(x, rounded=True)) - exact) <= out
+    for wrong in (muon.orthogonalize(x, steps=4), muon.orthogonalize(x, ns=[(0.9 * a, *muon.NS[1:])] * 5)):
+        assert norm(bf16(wrong) - exact) > out
