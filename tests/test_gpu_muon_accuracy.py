@@ -14,6 +14,7 @@ import torch
 
 import gradient_sync_zero_amd as G
 from oracle import muon as O
+from tests import test_gpu_muon as updates
 from tests.test_gpu_muon import f64, norm, run, workspace
 from tests.test_muon_accuracy import NAMES, U, matrix
 
@@ -46,3 +47,13 @@ def test_updates(rows, cols, name):
     got, exact = f64(plan.view(1, w)).reshape(rows, cols), O.orthogonalize(u)
     assert norm(got - exact) <= 2 * O.rounding_bound(u), norm(got - exact) / norm(exact)
     assert norm(got - O.orthogonalize(u, rounded=True)) <= O.rounding_bound(u)
+
+
+# panels in both orientations, of one matrix and several; pairs of steps in both
+@pytest.mark.parametrize("rows,cols,numel,tensors", [
+    (300, 100, [5, 30000, 30000], [2, 1]), (100, 300, [30000, 3], [0]), (33, 2049, [67617, 9, 67617, 67617], [0, 3, 2]),
+    (1000, 128, [128000], [0]), (140, 1200, [7, 168000, 168000], [1, 2]), (1200, 140, [168000, 1], [0])])
+@pytest.mark.parametrize("nesterov", [True, False])
+def test_update_with_a_long_side(rows, cols, numel, tensors, nesterov):
+    """As tests/test_gpu_muon.py's updates: momentum bit for bit, weights, parameters, and what lies around."""
+    updates.test_update(rows, cols, numel, tensors, nesterov)
