@@ -410,7 +410,11 @@ int gsz_adamw_step(float* master, float* m, float* v, const float* g, int64_t n,
  *   ws (device, 16-byte aligned, >= gsz_muon_workspace_bytes): scratch apart from x and out,
  *     per call in flight (two captured graphs that may run at once need one each); may be NULL
  *     where none is needed.
- * Deterministic.  GSZ_ERR_SIZE if rows or cols is over 2^17, a matrix over 2^32 elements, all of
+ * No atomics: the same call gives the same bits.  Matrices go 256 at a time (fewer where that is
+ * 2^33 elements), the rest at the end, and whether steps go two at a time and where sums are cut
+ * depends on how many go together: a matrix that needs a workspace has, in a call of another count or
+ * at another place in it, the same result within the errors above but not always the same bits.
+ * GSZ_ERR_SIZE if rows or cols is over 2^17, a matrix over 2^32 elements, all of
  * them over 1e15, count over 2^31 or the workspace too small. */
 int gsz_orthogonalize(const void* x, int32_t type, int64_t count, int64_t rows, int64_t cols,
                       int32_t steps, const double* ns, double eps, uint16_t* out, void* ws,
@@ -449,7 +453,8 @@ typedef struct gsz_muon_hp {
  *   master, momentum, g (device, flat_len fp32), params (device, flat_len bf16): the plan's
  *     flat layout (g as gsz_allreduce_mean leaves it); no two may overlap.
  *   coef (device float, from gsz_clip_coef); ws as gsz_orthogonalize's.
- * Ranks that share the work each list matrices of their own and gather the results. */
+ * Ranks that share the work each list matrices of their own and gather the results; a rank that
+ * works a matrix out again gets the gathered bits from the same list alone (gsz_orthogonalize). */
 int gsz_muon_step(const gsz_plan* plan, const int32_t* tensors, int32_t count, int64_t rows,
                   int64_t cols, float* master, float* momentum, const float* g, const float* coef,
                   const gsz_muon_hp* hp, uint16_t* params, void* ws, size_t ws_bytes,

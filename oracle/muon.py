@@ -12,8 +12,17 @@ def _half(v, scale):
     return (v * scale).astype(np.float16).astype(np.float64) / scale
 
 
+def group_of(rows, cols, count, index=0):
+    """How many matrices matrix `index` of a call's `count` goes with: 256 at a time, fewer where they
+    would have more than 2^33 elements (sides rounded up to 64), the rest at the end."""
+    padded = -(-rows // 64) * 64 * (-(-cols // 64) * 64)
+    most = max(1, min(256, 2 ** 33 // padded))
+    return min(most, count - index // most * most)
+
+
 def in_pairs(rows, cols, count=1):
-    """Whether the library takes two steps at once (X <- S1 S0 X, A1 = S0 A0 S0) for `count` matrices."""
+    """Whether the library takes two steps at once (X <- S1 S0 X, A1 = S0 A0 S0) for a group of `count`
+    matrices."""
     m, n = min(rows, cols), max(rows, cols)
     saved = count * m * m * (n - m)
     return m > 128 and (n >= 8 * m or (2 * n >= 5 * m and saved >= 1 << 30) or (2 * n >= 3 * m and saved >= 1 << 33))
@@ -29,13 +38,13 @@ def launches(steps, pairs):
         k += many
 
 
-def orthogonalize(x, steps=5, ns=None, eps=1e-7, rounded=False, count=1):
+def orthogonalize(x, steps=5, ns=None, eps=1e-7, rounded=False, count=1, index=0):
     """X = x / (|x| + eps); steps times A = X X^T, X = S X with S = a I + b A + c A A, from the
     smaller side.  rounded: X, A and S (and what a pair of steps adds) are rounded to fp16 where the
-    library rounds them in a call of `count` such matrices."""
+    library rounds them in matrix `index` of a call of `count`."""
     x = np.asarray(x, dtype=np.float64)
     if x.shape[0] > x.shape[1]:
-        return orthogonalize(x.T, steps, ns, eps, rounded, count).T
+        return orthogonalize(x.T, steps, ns, eps, rounded, count, index).T
     x = x / (np.sqrt((x * x).sum()) + eps)
     half = _half if rounded else lambda v, scale: v
 
@@ -43,7 +52,7 @@ def orthogonalize(x, steps=5, ns=None, eps=1e-7, rounded=False, count=1):
         a, b, c = NS if ns is None else ns[k]
         return half(a * np.eye(len(A)) + b * A + c * (A @ A), SCALE_A)
 
-    for k, many in launches(steps, rounded and in_pairs(*x.shape, count)):
+    for k, many in launches(steps, rounded and in_pairs(*x.shape, group_of(*x.shape, count, index))):
         if rounded:
             x = _half(x.astype(np.float32), SCALE_X)
         A = half(x @ x.T, SCALE_A)
@@ -55,7 +64,7 @@ def orthogonalize(x, steps=5, ns=None, eps=1e-7, rounded=False, count=1):
     return x
 
 
-def rounding_bound(x, steps=5, ns=None, eps=1e-7, count=1):
+def rounding_bound(x, steps=5, ns=None, eps=1e-7, count=1, index=0):
     """How far (2-norm) the fp16 roundings take the result: the root of the mean square over roundings,
     to first order.  What a call gives is 0.6 to 0.75 of it where many values are rounded (they lie anywhere
     between powers of two) and can be 1.8 times it where there is one.
@@ -84,7 +93,7 @@ def rounding_bound(x, steps=5, ns=None, eps=1e-7, count=1):
         return r2 * (values ** 2).sum() / m ** 2
 
     same, anti, outside = np.zeros((m, m)), np.zeros((m, m)), np.zeros(m)    # mean squares of X's error
-    for k, many in launches(steps, in_pairs(m, n, count)):
+    for k, many in launches(steps, in_pairs(m, n, group_of(m, n, count, index))):
         e = r2 * (s * s).sum() / (m * n)
         same, anti, outside = same + e / 2, anti + e / 2, outside + (n - m) * e
         s0, ea = s, rounding(s * s)

@@ -57,3 +57,30 @@ def test_updates(rows, cols, name):
 def test_update_with_a_long_side(rows, cols, numel, tensors, nesterov):
     """As tests/test_gpu_muon.py's updates: momentum bit for bit, weights, parameters, and what lies around."""
     updates.test_update(rows, cols, numel, tensors, nesterov)
+
+
+def test_how_a_matrix_goes_depends_on_its_group():
+    """Of 257 matrices of 129 x 400 the first 256 take steps in pairs and the last, alone, does not.  The
+    update's O is fp32: nearer to the oracle with the same roundings (1e-3, tests/test_gpu_muon.py) than
+    to the other one, and the last matrix has the bits it has by itself."""
+    rows, cols, count = 129, 400, 257
+    n = rows * cols
+    plan = G.Plan([n] * count, 1 << 40, 1)
+    g = torch.from_numpy(np.random.default_rng(1).normal(size=plan.flat_len).astype(np.float32)).cuda()
+    hp = G.make_muon_hp(lr=1.0, momentum=0.0, scale=-1.0, nesterov=False)
+
+    def update(tensors):
+        w, m = torch.zeros_like(g), torch.zeros_like(g)
+        p = torch.zeros(plan.flat_len, dtype=torch.bfloat16, device="cuda")
+        G.muon_step(plan, tensors, rows, cols, w, m, g, torch.ones(1, device="cuda"), hp, p, workspace(len(tensors), rows, cols))
+        return w
+
+    w = update(range(count))
+    assert torch.equal(plan.view(count - 1, update([count - 1])), plan.view(count - 1, w))
+    for t in (0, 255, 256):
+        u, got = f64(plan.view(t, g)).reshape(rows, cols), f64(plan.view(t, w)).reshape(rows, cols)
+        as_paired, as_single = O.orthogonalize(u, rounded=True, count=256), O.orthogonalize(u, rounded=True)
+        same, other = (as_single, as_paired) if t == 256 else (as_paired, as_single)
+        assert np.array_equal(O.orthogonalize(u, rounded=True, count=count, index=t), same)
+        assert norm(got - same) <= 1e-3 * norm(same)
+        assert norm(got - same) < norm(got - other)

@@ -4,6 +4,7 @@ step of bf16 more for bf16 ones)."""
 import numpy as np
 import pytest
 
+import gradient_sync_zero_amd as G
 from oracle import muon
 
 U = 2.0 ** -8
@@ -103,3 +104,21 @@ def test_a_mistake_is_seen_in_other_spectra(name):
     assert norm(bf16(muon.orthogonalize(x, rounded=True)) - exact) <= out
     for wrong in (muon.orthogonalize(x, steps=4), muon.orthogonalize(x, ns=[(0.9 * a, *muon.NS[1:])] * 5)):
         assert norm(bf16(wrong) - exact) > out
+
+
+def test_groups():
+    """How many matrices go together, and so whether in pairs, as the library's host half has it: a
+    workspace grows with the group alone, and holds the pairs' matrix where there are any."""
+    assert [muon.group_of(129, 400, 257, k) for k in (0, 255, 256)] == [256, 256, 1]
+    assert [muon.group_of(2 ** 17, 2 ** 14, 9, k) for k in (0, 3, 4, 8)] == [4, 4, 4, 1]
+    assert muon.group_of(65536, 65536, 5) == 2 and muon.group_of(3, 2, 1) == 1
+    assert muon.in_pairs(129, 400, 256) and not muon.in_pairs(129, 400, 1)
+    size = lambda *a: G.muon_workspace_bytes(*a)  # noqa: E731
+    assert size(255, 129, 400) < size(256, 129, 400) == size(257, 129, 400) == size(10 ** 6, 129, 400)
+    assert size(3, 2 ** 17, 2 ** 14) < size(4, 2 ** 17, 2 ** 14) == size(9, 2 ** 17, 2 ** 14)
+
+
+def test_a_matrix_behind_the_first_groups():
+    x = matrix(129, 400, "random")
+    first, last, alone = (muon.orthogonalize(x, rounded=True, **kw) for kw in (dict(count=257), dict(count=257, index=256), {}))
+    assert np.array_equal(last, alone) and not np.array_equal(first, last)
