@@ -396,10 +396,23 @@ int gsz_adamw_step(float* master, float* m, float* v, const float* g, int64_t n,
  * and 2^12, so the iterates' singular values must stay below 4 and the polynomial's values
  * below 16 (the usual coefficients keep them below 1.3 and 3.5).  Where one side is well
  * longer (how much goes by the sizes and by count) two steps are worked out together, X <- (S' S) X
- * with A' = S A S, and the product's values must stay below 256.  Of the exact result (2-norm, bf16's own rounding included) out is off by 0.2% for
- * matrices of random elements, by up to 0.3% for small ones, 0.5% and 1% where the singular values
- * fall evenly to 1e-3 and 1e-6 of the largest; directions that x does not have at all but for
- * rounding grow by 3.4 a step, so a matrix of rank one can be off by 15%.  A matrix of zeros gives zeros; one with a
+ * with A' = S A S, and the product's values must stay below 256.
+ * Of the exact result (2-norm) out is off by its own rounding to bf16, 0.17%, and by those to fp16.
+ * These are 0.1% where all singular values are alike in size, but a step multiplies what is small by
+ * 3.4445, a rounding in a direction that x does not have as well, so they weigh more the fewer
+ * directions x has.  After five of the usual steps, both together, at most:
+ *                                  smaller side from 64 on   16 to 63
+ *   random elements                          0.25%             0.4%
+ *   singular values that fall evenly
+ *     to 1e-3 of the largest                 1%                2%
+ *     to 1e-6                                2%                3%
+ *   equal ones, the others zero:
+ *     32 of them                             3%
+ *     16                                     5%                4% (32 to 63)
+ *     8                                      4.5%              4.5%
+ *     4                                      8.5%              8.5%
+ *     one                                   16%               16%
+ * (below 16: random elements 0.6%, the others up to 16%).  A matrix of zeros gives zeros; one with a
  * value that is not finite gives NaN everywhere, the others of the call unaffected.
  *   x (device, count * rows * cols values of `type`, GSZ_TYPE_BF16 or GSZ_TYPE_F32, row by
  *     row, one matrix after the other; any multiple of the value's size).

@@ -122,3 +122,38 @@ def test_a_matrix_behind_the_first_groups():
     x = matrix(129, 400, "random")
     first, last, alone = (muon.orthogonalize(x, rounded=True, **kw) for kw in (dict(count=257), dict(count=257, index=256), {}))
     assert np.array_equal(last, alone) and not np.array_equal(first, last)
+
+
+# What include/gsz.h states of five steps: parts of the exact result, its rounding to bf16 included.
+STATED = {"random": (0.0025, 0.004), "1e-3": (0.01, 0.02), "1e-6": (0.02, 0.03), "32": (0.03, None), "16": (0.05, 0.04), "8": (0.045, 0.045),
+          "4": (0.085, 0.085), "1": (0.16, 0.16)}
+
+
+def stated(rows, cols, name):
+    """The limit for a matrix of these sizes, or None where none is stated."""
+    m = min(rows, cols)
+    if m < 16:
+        return 0.006 if name == "random" else 0.16
+    limit = STATED[name][m < 64]
+    return None if name == "16" and m < 32 else limit
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 40), (2, 3), (4, 4), (12, 30), (17, 64), (60, 60), (33, 2049), (60, 100), (64, 64), (128, 128), (160, 200),
+                                       (140, 1200), (500, 200), (300, 2400), (512, 512)])
+def test_the_stated_accuracy(rows, cols):
+    for name in STATED:
+        if name != "random" and (min(rows, cols) < 3 or name.isdigit() and int(name) >= min(rows, cols)) or stated(rows, cols, name) is None:
+            continue
+        for seed in range(3):
+            x = matrix(rows, cols, name, seed)
+            exact = muon.orthogonalize(x)
+            off = norm(bf16(muon.orthogonalize(x, rounded=True)) - exact) / norm(exact)
+            assert off <= stated(rows, cols, name), (name, seed, off)
+
+
+def test_positive_rank_one():
+    rng = np.random.default_rng(3)
+    for rows, cols in ((128, 128), (140, 1200), (300, 2400)):
+        x = np.outer(rng.uniform(0.1, 1, rows), rng.uniform(0.1, 1, cols)).astype(np.float32)
+        exact = muon.orthogonalize(x)
+        assert norm(bf16(muon.orthogonalize(x, rounded=True)) - exact) <= 0.16 * norm(exact)
