@@ -14,12 +14,17 @@ namespace {
 // 16 bytes a lane from the descriptor's base + offset + uniform to LDS, lane l's at lds + 16 l.
 // In assembly because the compiler, which cannot tell which LDS reads a builtin load concerns
 // where they are the transposing ones, would wait for it before the next of them.  There is
-// no result register; whoever reads the LDS calls loads_landed first.
+// no result register; whoever reads the LDS calls loads_landed first.  m0 is named as changed, so that no
+// value of the compiler's is taken to outlive the statement there; it says that it keeps none in
+// reserved registers across such a one, which is what is wanted.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_to_lds(BufRes res, _Float16* lds, int offset, int uniform) {
     const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 : : "s"(at), "v"(offset), "s"(res), "s"(uniform) : "memory");
+                 : : "s"(at), "v"(offset), "s"(res), "s"(uniform) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 // All but the last PENDING of this wave's loads to LDS are there.
 template <int PENDING>
 __device__ __forceinline__ void loads_landed() {
