@@ -412,7 +412,9 @@ int gsz_adamw_step(float* master, float* m, float* v, const float* g, int64_t n,
  *     8                                      4.5%              4.5%
  *     4                                      8.5%              8.5%
  *     one                                   16%               16%
- * (below 16: random elements 0.6%, the others up to 16%).  A matrix of zeros gives zeros; one with a
+ * (below 16: random elements 0.6%, the others up to 16%).  With an eps far above |x|
+ * the elements of X below 2^-27 lose bits, and below 2^-38 all: then out is off by up to 3e-9
+ * sqrt(rows cols) besides.  A matrix of zeros gives zeros; one with a
  * value that is not finite gives NaN everywhere, the others of the call unaffected.
  *   x (device, count * rows * cols values of `type`, GSZ_TYPE_BF16 or GSZ_TYPE_F32, row by
  *     row, one matrix after the other; any multiple of the value's size).
@@ -464,7 +466,10 @@ typedef struct gsz_muon_hp {
  *     otherwise), none of them twice (GSZ_ERR_INVALID_ARG).  The plan's device tables are
  *     not used: it need not be uploaded.
  *   master, momentum, g (device, flat_len fp32), params (device, flat_len bf16): the plan's
- *     flat layout (g as gsz_allreduce_mean leaves it); no two may overlap.
+ *     flat layout (g as gsz_allreduce_mean leaves it); no two may overlap.  They are the plan's
+ *     whole buffers: a matrix is orthogonalised as a whole, so the shards that gsz_shard_reduce_mean
+ *     and gsz_shard_adamw_step work on do not do.  Where state is to be spread over ranks, each
+ *     rank's matrices make a plan of their own.
  *   coef (device float, from gsz_clip_coef); ws as gsz_orthogonalize's.
  * Ranks that share the work each list matrices of their own and gather the results; a rank that
  * works a matrix out again gets the gathered bits from the same list alone (gsz_orthogonalize). */

@@ -16,7 +16,7 @@ import gradient_sync_zero_amd as G
 from oracle import muon as O
 from tests import test_gpu_muon as updates
 from tests.test_gpu_muon import f64, norm, run, workspace
-from tests.test_muon_accuracy import STATED, U, matrix, stated
+from tests.test_muon_accuracy import STATED, U, far_eps, matrix, stated
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +86,12 @@ def test_how_a_matrix_goes_depends_on_its_group():
         assert np.array_equal(O.orthogonalize(u, rounded=True, count=count, index=t), same)
         assert norm(got - same) <= 1e-3 * norm(same)
         assert norm(got - same) < norm(got - other)
+
+
+@pytest.mark.parametrize("eps", [1.0, 1e3, 1e6, 1e9, 1e12])
+@pytest.mark.parametrize("rows,cols", [(40, 60), (90, 400), (140, 300)])
+def test_eps_far_above_the_norm(rows, cols, eps):
+    x = matrix(rows, cols, "random")
+    x = torch.from_numpy(x / np.float32(norm(x))).cuda()
+    exact, bound = far_eps(f64(x), eps)
+    assert norm(f64(run(x, eps=eps)) - exact) <= bound

@@ -157,3 +157,22 @@ def test_positive_rank_one():
         x = np.outer(rng.uniform(0.1, 1, rows), rng.uniform(0.1, 1, cols)).astype(np.float32)
         exact = muon.orthogonalize(x)
         assert norm(bf16(muon.orthogonalize(x, rounded=True)) - exact) <= 0.16 * norm(exact)
+
+
+def far_eps(x, eps):
+    """How far the result may be off where eps is far above |x|, and fp16 has no full precision: each
+    of the 5 roundings of X is off by 2^-38 an element, grown by a = 3.4445 a step; X elsewhere and S by 2^-11
+    of their values, and the output by its own rounding."""
+    exact = muon.orthogonalize(x, eps=eps)
+    absolute = 2.0 ** -38 * sum(muon.NS[0] ** k for k in range(1, 6))
+    assert absolute < 3e-9
+    return exact, absolute * np.sqrt(x.size) + (10 * 2.0 ** -11 + U) * norm(exact)
+
+
+@pytest.mark.parametrize("eps", [1.0, 1e3, 1e6, 1e9, 1e12])
+@pytest.mark.parametrize("rows,cols", [(40, 60), (140, 300)])
+def test_eps_far_above_the_norm(rows, cols, eps):
+    x = matrix(rows, cols, "random")
+    x = (x / norm(x)).astype(np.float32)
+    exact, bound = far_eps(x, eps)
+    assert norm(bf16(muon.orthogonalize(x, eps=eps, rounded=True)) - exact) <= bound
