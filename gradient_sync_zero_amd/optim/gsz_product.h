@@ -19,9 +19,10 @@
 // k is a multiple of 64: operands are padded with zeros, which the products keep.  Rows past
 // an operand's end are read as zeros (its descriptor's range ends there) and not written.
 //
-// 8192 x 8192 x 8192: 840 to 855 us, 1.29 to 1.31 PFLOP/s.  The matrix cores are busy for 72% of the time
-// and the clock is down to 1.63 to 1.73 GHz under their load; LDS, 128 bytes a clock, is the next
-// bound.  Measured and not kept: blocks that stay and run their loads on into the next tile
+// 8192 x 8192 x 8192: 840 to 870 us, 1.26 to 1.31 PFLOP/s.  The matrix cores are busy for 73 to 75% of the
+// time and the clock is down to 1.63 GHz under their load; LDS, 128 bytes a clock, is the next bound.
+// (24 of 2048 x 2048 x 2048: 55% at 1.93 GHz, of a symmetric result 39 to 44% at 2.05: the ends of 32
+// steps of k, tiles over the diagonal and rounds that are not full.)  Measured and not kept: blocks that stay and run their loads on into the next tile
 // (24 of 2048 x 2048 x 2048 401 us against 396), 128 x 128 a wave (its sums spill: half the
 // speed), four tiles of 128 in LDS with one block a CU (27.6 us against 28.3 and 14.0 against 13.3).
 #pragma once
